@@ -118,7 +118,8 @@ typedef struct {
 typedef enum {
   SSM_FLAG_ZOH_EXACT = 1,
   SSM_FLAG_SAVE_STATES = 2,
-  SSM_FLAG_TOKEN_MAJOR = 4
+  SSM_FLAG_TOKEN_MAJOR = 4,
+  SSM_FLAG_UNTIED = 8 /* gated scan only: the input enters as given (see ssm_gated_scan_fwd) */
 } ssm_flags;
 
 /* SSM_FLAG_TOKEN_MAJOR: u, delta, z and y (and, in ssm_scan_bwd, dout, du,
@@ -296,6 +297,118 @@ ssm_status ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int
                                  const void *dout, void *dx, float *dweight, float *dbias,
                                  float *dinitial_state, ssm_stream_t stream);
 
+/* Gated linear recurrence: one state per channel, its forget gate a sigmoid of
+ * an input, run as a scan over whole sequences.  The reading guide's gating
+ * reduction of the selective scan ("O Mecanismo de Selecao (S6)": N = 1,
+ * A = -1, B = 1 gives h_t = (1 - g_t) h_{t-1} + g_t x_t with a sigmoid gate),
+ * as an operator of its own:
+ *   g_t = sigmoid(-(f_t + f_bias)),  a_t = 1 - g_t = sigmoid(f_t + f_bias)
+ *   h_t = a_t h_{t-1} + g_t u_t        (default: the gates are tied)
+ *   h_t = a_t h_{t-1} + u_t            (SSM_FLAG_UNTIED: u_t already gated)
+ *   y_t = h_t * SiLU(z_t)
+ * Layouts as in ssm_scan_fwd (SSM_FLAG_TOKEN_MAJOR included, here for every
+ * dtype and dim):
+ *   u, f, z, y                 [batch][dim][seqlen] io dtype
+ *   f_bias                     [dim] fp32, nullable
+ *   starts                     [batch][seqlen] bytes, nullable: where nonzero a
+ *                              packed sequence starts, and h_{t-1} counts as 0
+ *                              whatever it is (infinities and NaN included; at
+ *                              t = 0 initial_state is dropped)
+ *   initial_state, last_state  [batch][dim] fp32, nullable (zeros; not written)
+ * z is nullable (no output gate).  shape->dstate must be 1 and lanes 0; flags
+ * may hold TOKEN_MAJOR, SAVE_STATES and UNTIED.  path: PER_GROUP walks each
+ * channel's sequence in one warp (channel-major only); LOOKBACK splits every
+ * sequence into time tiles that hand their states on through the workspace
+ * with a bounded wait; AUTO picks; the others return SSM_ERR_UNSUPPORTED.
+ * f = +inf leaves the state as it was (a padded step, tied), f = -inf forgets
+ * it.  The order of every sum is fixed: repeated calls give equal bits.
+ * y may not alias an input.  seqlen 0 copies initial_state to last_state.
+ *
+ * The workspace (256-byte aligned) holds the saved states and the look-back
+ * schedule's states; NULL is accepted where the query below gives 0. */
+ssm_status ssm_gated_scan_fwd(const ssm_shape *shape, const void *u, const void *f,
+                              const void *z, const float *f_bias, const uint8_t *starts,
+                              const float *initial_state, void *y, float *last_state,
+                              void *workspace, size_t ws_bytes, ssm_stream_t stream);
+
+/* Bytes of workspace ssm_gated_scan_fwd / _bwd need on the current device; 0
+ * where none is needed and for an invalid shape. */
+size_t ssm_gated_scan_fwd_workspace_bytes(const ssm_shape *shape);
+size_t ssm_gated_scan_bwd_workspace_bytes(const ssm_shape *shape);
+
+/* Path AUTO would choose for `shape` in the forward on the current device;
+ * SSM_PATH_AUTO itself for an invalid shape. */
+int32_t ssm_gated_scan_path(const ssm_shape *shape);
+
+/* Backward of ssm_gated_scan_fwd: gradients of sum(dout * y) +
+ * sum(dlast_state * last_state), the states recomputed from the inputs.
+ *  fwd_workspace   nullable: the workspace of a forward of the same shape,
+ *                  inputs and flags, with SSM_FLAG_SAVE_STATES (which this
+ *                  shape must carry too); without it the backward first
+ *                  recomputes the saved states
+ *  dlast_state     [batch][dim] fp32, nullable
+ *  du, df, dz      as u, f, z (overwritten); dz exactly when z is given
+ *  df_bias         [dim] fp32, exactly when f_bias is given
+ *  dinitial_state  [batch][dim] fp32, nullable
+ * No gradient passes a start.  No atomics on results: bitwise repeatable.
+ * du, df and dz may not alias an input or one another. */
+ssm_status ssm_gated_scan_bwd(const ssm_shape *shape, const void *u, const void *f,
+                              const void *z, const float *f_bias, const uint8_t *starts,
+                              const float *initial_state, const void *dout,
+                              const float *dlast_state, const void *fwd_workspace,
+                              void *du, void *df, void *dz, float *df_bias,
+                              float *dinitial_state, void *workspace, size_t ws_bytes,
+                              ssm_stream_t stream);
+
+/* One token of the gated recurrence for every (batch, channel): state
+ * [batch][dim] fp32 is read and overwritten; u, f, z, y [batch][dim].
+ * shape->seqlen must be 1; path must be AUTO; flags may hold UNTIED
+ * (TOKEN_MAJOR is ignored, SAVE_STATES is SSM_ERR_UNSUPPORTED).  No workspace.
+ * y and state must not alias another argument. */
+ssm_status ssm_gated_scan_step(const ssm_shape *shape, const void *u, const void *f,
+                               const void *z, const float *f_bias, float *state, void *y,
+                               ssm_stream_t stream);
+
+/* Layer norm over the last axis, with the residual stream's addition before it
+ * (the residual connection around the Mamba block, "O que e um modelo Mamba?",
+ * ibm.com, the block walk-through), per row of dim values:
+ *   s = x + residual  rounded to residual_dtype   (s = x without residual)
+ *   y = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps) * weight + bias
+ * What is normalised is s as stored, so that the backward sees the same values.
+ *  x, y                    [rows][dim] io dtype
+ *  residual, residual_out  [rows][dim] residual_dtype (io_dtype or fp32); both
+ *                          given or both NULL; residual_out may be residual
+ *  weight, bias            [dim] fp32; bias nullable
+ * eps >= 0.  Sums and statistics are fp32, the variance formed from the
+ * centred values.  y may not alias an input; residual_out may not alias x. */
+ssm_status ssm_layer_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t residual_dtype,
+                          const void *x, const void *residual, const float *weight,
+                          const float *bias, float eps, void *y, void *residual_out,
+                          ssm_stream_t stream);
+
+/* Bytes of workspace ssm_layer_norm_bwd needs on the current device (per-block
+ * partial sums of dweight and dbias); 0 for invalid sizes. */
+size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
+/* Backward of ssm_layer_norm; the statistics are recomputed from s.
+ *  s               [rows][dim] residual_dtype: what was normalised (the
+ *                  forward's residual_out, or x itself with residual_dtype =
+ *                  io_dtype)
+ *  dy              [rows][dim] io dtype
+ *  dresidual_out   [rows][dim] residual_dtype, nullable: the gradient that
+ *                  reaches s past the norm, added to the norm's
+ *  dx              [rows][dim] io dtype
+ *  dresidual       [rows][dim] residual_dtype: the gradient of s unrounded to
+ *                  the io dtype; given exactly when residual_dtype differs from
+ *                  io_dtype (else dx is it); may be dresidual_out
+ *  dweight         [dim] fp32; dbias [dim] fp32, nullable
+ * No atomics on results: bitwise repeatable.  dx may not alias an input. */
+ssm_status ssm_layer_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32_t residual_dtype,
+                              const void *s, const float *weight, float eps, const void *dy,
+                              const void *dresidual_out, void *dx, void *dresidual,
+                              float *dweight, float *dbias, void *workspace, size_t ws_bytes,
+                              ssm_stream_t stream);
+
 /* Synchronises `stream`, reads and clears the device error word of
  * `workspace`.  SSM_OK, SSM_ERR_DEVICE_TIMEOUT or SSM_ERR_CUDA. */
 ssm_status ssm_scan_check(void *workspace, ssm_stream_t stream);
@@ -310,7 +423,8 @@ ssm_status ssm_scan_test_wait_timeout(void *workspace, size_t ws_bytes,
 
 /* Test hook for callers' error paths: the next `count` calls of
  * ssm_scan_fwd, ssm_scan_bwd, ssm_scan_step, ssm_causal_conv1d and
- * ssm_causal_conv1d_bwd (ssm_scan_fwd_noalloc included) that pass their
+ * ssm_causal_conv1d_bwd (ssm_scan_fwd_noalloc included), and of the
+ * ssm_gated_scan_* and ssm_layer_norm* operators, that pass their
  * argument and workspace checks return SSM_ERR_CUDA as if their first launch
  * had failed with cudaErrorLaunchFailure; they launch nothing and leave every
  * buffer untouched.  count <= 0 disarms it.  Process-wide, thread-safe;

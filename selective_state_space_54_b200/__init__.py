@@ -9,6 +9,12 @@ kernels (include/ssm_scan.h).  There is no CPU path.
     grads = scan_bwd(u, delta, A, B, C, D, z, delta_bias, dout)
     y_t = scan_step(u_t, delta_t, A, B_t, C_t, D, z_t, delta_bias, state=state)
 
+    y, last = gated_scan_fwd(u, f, z, f_bias, return_last_state=True)
+    grads = gated_scan_bwd(u, f, z, f_bias, dout)
+    y_t = gated_scan_step(u_t, f_t, z_t, f_bias, state=state)
+    y, residual = layer_norm(x, weight, bias, residual=residual)
+    grads = layer_norm_bwd(residual, weight, bias, dy, dresidual_out=dresidual)
+
 Layouts: u, delta, z, y, dout (batch, dim, seqlen); B, C (batch, seqlen,
 dstate); A (dim, dstate) fp32; D, delta_bias (dim,) fp32; states (batch, dim,
 dstate) fp32.  io tensors are all bf16 or all fp32.
@@ -20,12 +26,14 @@ import functools
 
 from . import _lib
 from ._lib import (PATH_NAMES, SSM_BF16, SSM_F32, SSM_FLAG_SAVE_STATES,  # noqa: F401
-                   SSM_FLAG_TOKEN_MAJOR, SSM_FLAG_ZOH_EXACT, SSM_PATH_AUTO,
+                   SSM_FLAG_TOKEN_MAJOR, SSM_FLAG_UNTIED, SSM_FLAG_ZOH_EXACT, SSM_PATH_AUTO,
                    SSM_PATH_LOOKBACK, SSM_PATH_LOOKBACK_WS, SSM_PATH_PER_GROUP, SSM_PATH_SPLIT_L,
                    ssm_shape)
 
 __all__ = ["scan_fwd", "scan_bwd", "scan_step", "causal_conv1d", "causal_conv1d_bwd", "fwd_workspace_bytes", "bwd_workspace_bytes",
-           "fwd_path", "check", "ScanError", "make_shape"]
+           "gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "gated_scan_shape", "gated_scan_path",
+           "gated_scan_fwd_workspace_bytes", "gated_scan_bwd_workspace_bytes", "layer_norm", "layer_norm_bwd",
+           "layer_norm_bwd_workspace_bytes", "fwd_path", "check", "ScanError", "make_shape"]
 
 
 class ScanError(RuntimeError):
@@ -296,6 +304,304 @@ def scan_bwd(u, delta, A, B, C, D, z, delta_bias, dout, *, delta_softplus=True,
         _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream))
     if rc != 0:
         raise ScanError(rc, "ssm_scan_bwd")
+    return g
+
+
+# ---- gated linear recurrence and layer norm ------------------------------------
+class _launch:
+    """The stream a call launches on, as ``with _launch(device, stream) as handle:``:
+    the caller's, or the current one of the tensors' own device.  The device is made
+    current for the launch, and what the call allocates belongs to that stream."""
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, None
+
+    def __enter__(self):
+        import torch
+        if self.stream is None:
+            if torch.cuda.current_device() != self.device.index:
+                self.guards = torch.cuda.device(self.device)
+                self.guards.__enter__()
+            return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+        if self.stream.device != self.device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
+        self.guards = torch.cuda.stream(self.stream)
+        self.guards.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guards is not None:
+            self.guards.__exit__(*exc)
+
+
+def _cuda_device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _workspace_for(nbytes, device, workspace):
+    """A caller's workspace checked, or a new one; None where none is needed."""
+    import torch
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if not workspace.is_cuda or workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.nbytes < nbytes:
+        raise ValueError(f"workspace holds {workspace.nbytes} bytes, needs {nbytes}")
+    return workspace
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_shape(batch, dim, seqlen, io_dtype, path, flags):
+    # read-only for the library (a const pointer): one struct serves every call of a shape
+    return make_shape(batch, dim, seqlen, 1, io_dtype, path, flags=flags)
+
+
+def gated_scan_shape(u, *, tied=True, save_states=False, token_major=False, path: int = SSM_PATH_AUTO) -> ssm_shape:
+    """The shape of a gated_scan_fwd / gated_scan_bwd call on ``u``, for the workspace queries."""
+    if u.dim() != 3:
+        raise ValueError(f"u has shape {tuple(u.shape)}, expected three axes")
+    batch, seqlen, dim = u.shape if token_major else (u.shape[0], u.shape[2], u.shape[1])
+    flags = ((0 if tied else SSM_FLAG_UNTIED) | (SSM_FLAG_SAVE_STATES if save_states else 0)
+             | (SSM_FLAG_TOKEN_MAJOR if token_major else 0))
+    return _gated_shape(batch, dim, seqlen, _io_dtype(u), path, flags)
+
+
+def gated_scan_fwd_workspace_bytes(shape: ssm_shape) -> int:
+    return int(_lib.load().ssm_gated_scan_fwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def gated_scan_bwd_workspace_bytes(shape: ssm_shape) -> int:
+    return int(_lib.load().ssm_gated_scan_bwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def gated_scan_path(shape: ssm_shape) -> str:
+    return PATH_NAMES[int(_lib.load().ssm_gated_scan_path(ctypes.byref(shape)))]
+
+
+def _check_starts(starts, batch, seqlen, dev):
+    import torch
+    if starts is None:
+        return None
+    if starts.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"starts has dtype {starts.dtype}, expected bool or uint8")
+    _check_io("starts", starts, (batch, seqlen), starts.dtype, dev)
+    return starts
+
+
+def _check_gated(shape, u, f, z, f_bias, starts, initial_state, token_major):
+    import torch
+    batch, dim, seqlen = shape.batch, shape.dim, shape.seqlen
+    dt, dev = u.dtype, u.device
+    act = u.shape
+    _check_io("u", u, act, dt, dev)
+    _check_io("f", f, act, dt, dev)
+    _check_io("z", z, act, dt, dev)
+    _check_io("f_bias", f_bias, (dim,), torch.float32, dev)
+    _check_io("initial_state", initial_state, (batch, dim), torch.float32, dev)
+    _check_starts(starts, batch, seqlen, dev)
+
+
+def gated_scan_fwd(u, f, z=None, f_bias=None, *, tied=True, starts=None, initial_state=None, y=None,
+                   last_state=None, return_last_state=False, workspace=None, path: int = SSM_PATH_AUTO,
+                   save_states=False, token_major=False, check_status=False, stream=None):
+    """Gated linear recurrence over whole sequences; returns y, or (y, last_state).
+
+    With a_t = sigmoid(f_t + f_bias): h_t = a_t h_{t-1} + (1 - a_t) u_t (``tied``) or
+    h_t = a_t h_{t-1} + u_t (``tied=False``: u is gated already), y_t = h_t SiLU(z_t).
+    u, f, z, y (batch, dim, seqlen), or (batch, seqlen, dim) with token_major; f_bias
+    (dim,) and the states (batch, dim) fp32.  starts (batch, seqlen), bool or uint8: a
+    packed sequence starts there, so h_{t-1} counts as 0 (initial_state too, at t = 0).
+    save_states writes the states gated_scan_bwd(fwd_workspace=...) needs into
+    ``workspace`` (which must then be given).  check_status: as in scan_fwd."""
+    import torch
+    dev = _cuda_device("u", u)
+    shape = gated_scan_shape(u, tied=tied, save_states=save_states, token_major=token_major, path=path)
+    _check_gated(shape, u, f, z, f_bias, starts, initial_state, token_major)
+    if save_states and workspace is None:
+        raise ValueError("save_states writes into the workspace: pass workspace=")
+    lib = _lib.load()
+    ref = ctypes.byref(shape)
+    with _launch(dev, stream) as handle:
+        if y is None:
+            y = torch.empty_like(u)
+        else:
+            _check_io("y", y, u.shape, u.dtype, dev)
+        if last_state is not None:
+            _check_io("last_state", last_state, (shape.batch, shape.dim), torch.float32, dev)
+        elif return_last_state:
+            last_state = torch.empty((shape.batch, shape.dim), dtype=torch.float32, device=dev)
+        nbytes = int(lib.ssm_gated_scan_fwd_workspace_bytes(ref))
+        ws = _workspace_for(nbytes, dev, workspace)
+        rc = lib.ssm_gated_scan_fwd(ref, _ptr(u), _ptr(f), _ptr(z), _ptr(f_bias), _ptr(starts), _ptr(initial_state),
+                                    _ptr(y), _ptr(last_state), _ptr(ws), 0 if ws is None else ws.nbytes, handle)
+        if rc != 0:
+            raise ScanError(rc, "ssm_gated_scan_fwd")
+        if check_status and nbytes:
+            check(ws, stream)
+    if return_last_state:
+        return y, last_state
+    return y
+
+
+def gated_scan_bwd(u, f, z, f_bias, dout, *, tied=True, starts=None, initial_state=None, dlast_state=None,
+                   want_dinitial_state=False, out=None, workspace=None, fwd_workspace=None,
+                   path: int = SSM_PATH_AUTO, token_major=False, check_status=False, stream=None):
+    """Backward of gated_scan_fwd by recomputation; returns a dict of the gradients
+    du, df, dz, df_bias, dinitial_state (None for what is absent).  dlast_state
+    (batch, dim) fp32: the gradient reaching last_state.  fwd_workspace: the workspace
+    of a gated_scan_fwd(save_states=True) call on the same inputs."""
+    import torch
+    dev = _cuda_device("u", u)
+    shape = gated_scan_shape(u, tied=tied, save_states=fwd_workspace is not None, token_major=token_major, path=path)
+    _check_gated(shape, u, f, z, f_bias, starts, initial_state, token_major)
+    batch, dim, f32 = shape.batch, shape.dim, torch.float32
+    _check_io("dout", dout, u.shape, u.dtype, dev)
+    _check_io("dlast_state", dlast_state, (batch, dim), f32, dev)
+    lib = _lib.load()
+    ref = ctypes.byref(shape)
+    if fwd_workspace is not None:
+        _workspace_for(int(lib.ssm_gated_scan_fwd_workspace_bytes(ref)), dev, fwd_workspace)
+    with _launch(dev, stream) as handle:
+        g = dict(out or {})
+        for k, like, shp, ty in (("du", u, u.shape, u.dtype), ("df", u, u.shape, u.dtype), ("dz", z, u.shape, u.dtype),
+                                 ("df_bias", f_bias, (dim,), f32),
+                                 ("dinitial_state", u if want_dinitial_state else None, (batch, dim), f32)):
+            if g.get(k) is not None:
+                _check_io(k, g[k], shp, ty, dev)
+            else:
+                g[k] = torch.empty(shp, dtype=ty, device=dev) if like is not None else None
+        ws = _workspace_for(int(lib.ssm_gated_scan_bwd_workspace_bytes(ref)), dev, workspace)
+        rc = lib.ssm_gated_scan_bwd(
+            ref, _ptr(u), _ptr(f), _ptr(z), _ptr(f_bias), _ptr(starts), _ptr(initial_state), _ptr(dout),
+            _ptr(dlast_state), _ptr(fwd_workspace), _ptr(g["du"]), _ptr(g["df"]), _ptr(g["dz"]), _ptr(g["df_bias"]),
+            _ptr(g["dinitial_state"]), _ptr(ws), 0 if ws is None else ws.nbytes, handle)
+        if rc != 0:
+            raise ScanError(rc, "ssm_gated_scan_bwd")
+        if check_status and ws is not None:
+            check(ws, stream)
+    return g
+
+
+def gated_scan_step(u, f, z=None, f_bias=None, *, state, tied=True, y=None, stream=None):
+    """One token of the gated recurrence for every (batch, channel): updates ``state``
+    (batch, dim) fp32 in place and returns y.  u, f, z, y (batch, dim)."""
+    import torch
+    dev = _cuda_device("u", u)
+    batch, dim = u.shape
+    dt = u.dtype
+    _check_io("u", u, (batch, dim), dt, dev)
+    _check_io("f", f, (batch, dim), dt, dev)
+    _check_io("z", z, (batch, dim), dt, dev)
+    _check_io("f_bias", f_bias, (dim,), torch.float32, dev)
+    _check_io("state", state, (batch, dim), torch.float32, dev)
+    shape = _gated_shape(batch, dim, 1, _io_dtype(u), SSM_PATH_AUTO, 0 if tied else SSM_FLAG_UNTIED)
+    with _launch(dev, stream) as handle:
+        if y is None:
+            y = torch.empty_like(u)
+        else:
+            _check_io("y", y, (batch, dim), dt, dev)
+        rc = _lib.load().ssm_gated_scan_step(ctypes.byref(shape), _ptr(u), _ptr(f), _ptr(z), _ptr(f_bias),
+                                             _ptr(state), _ptr(y), handle)
+    if rc != 0:
+        raise ScanError(rc, "ssm_gated_scan_step")
+    return y
+
+
+def _residual_dtype(name, t, io) -> int:
+    import torch
+    if t.dtype != io and t.dtype != torch.float32:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {io} or {torch.float32}")
+    return _io_dtype(t)
+
+
+def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, residual_out=None, stream=None):
+    """Layer norm over the last axis, with the residual stream's addition before it.
+
+    Without ``residual`` returns y = norm(x) * weight + bias.  With it returns (y, s):
+    s = x + residual, rounded to the residual's dtype (x's or fp32), and y = norm(s) *
+    weight + bias.  x, y (..., dim) bf16 or fp32; weight, bias (dim,) fp32.
+    residual_out may be residual itself."""
+    import torch
+    dev = _cuda_device("x", x)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one axis")
+    dt, dim = x.dtype, x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    io = rd = _io_dtype(x)
+    _check_io("x", x, x.shape, dt, dev)
+    _check_io("weight", weight, (dim,), torch.float32, dev)
+    _check_io("bias", bias, (dim,), torch.float32, dev)
+    if residual is not None:
+        rd = _residual_dtype("residual", residual, dt)
+        _check_io("residual", residual, x.shape, residual.dtype, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    with _launch(dev, stream) as handle:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check_io("y", y, x.shape, dt, dev)
+        if residual is not None:
+            if residual_out is None:
+                residual_out = torch.empty_like(residual)
+            else:
+                _check_io("residual_out", residual_out, x.shape, residual.dtype, dev)
+        rc = _lib.load().ssm_layer_norm(rows, dim, io, rd, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps,
+                                        _ptr(y), _ptr(residual_out), handle)
+    if rc != 0:
+        raise ScanError(rc, "ssm_layer_norm")
+    return y if residual is None else (y, residual_out)
+
+
+def layer_norm_bwd_workspace_bytes(rows: int, dim: int) -> int:
+    return int(_lib.load().ssm_layer_norm_bwd_workspace_bytes(rows, dim))
+
+
+def layer_norm_bwd(s, weight, bias, dy, *, eps=1e-5, dresidual_out=None, out=None, workspace=None, stream=None):
+    """Backward of layer_norm; returns dict(dx, dresidual, dweight, dbias).
+
+    s: what was normalised (layer_norm's second result, or x where there was no
+    residual), whose dtype is dy's or fp32; dresidual_out: the gradient reaching s past
+    the norm, in s's dtype.  dx has dy's dtype; dresidual is the gradient of the
+    residual in s's dtype, the same tensor as dx where the two dtypes are one.  bias:
+    the forward's, or None for no dbias."""
+    import torch
+    dev = _cuda_device("dy", dy)
+    if dy.dim() < 1:
+        raise ValueError("dy needs at least one axis")
+    dt, dim, f32 = dy.dtype, dy.shape[-1], torch.float32
+    rows = dy.numel() // dim if dim else 0
+    io = _io_dtype(dy)
+    rd = _residual_dtype("s", s, dt)
+    _check_io("s", s, dy.shape, s.dtype, dev)
+    _check_io("dy", dy, dy.shape, dt, dev)
+    _check_io("weight", weight, (dim,), f32, dev)
+    _check_io("bias", bias, (dim,), f32, dev)
+    _check_io("dresidual_out", dresidual_out, dy.shape, s.dtype, dev)
+    lib = _lib.load()
+    with _launch(dev, stream) as handle:
+        g = dict(out or {})
+        for k, want, shp, ty in (("dx", True, dy.shape, dt), ("dresidual", io != rd, dy.shape, s.dtype),
+                                 ("dweight", True, (dim,), f32), ("dbias", bias is not None, (dim,), f32)):
+            if not want:
+                g[k] = None
+            elif g.get(k) is not None:
+                _check_io(k, g[k], shp, ty, dev)
+            else:
+                g[k] = torch.empty(shp, dtype=ty, device=dev)
+        ws = _workspace_for(int(lib.ssm_layer_norm_bwd_workspace_bytes(rows, dim)), dev, workspace)
+        rc = lib.ssm_layer_norm_bwd(rows, dim, io, rd, _ptr(s), _ptr(weight), eps, _ptr(dy), _ptr(dresidual_out),
+                                    _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
+                                    _ptr(ws), 0 if ws is None else ws.nbytes, handle)
+    if rc != 0:
+        raise ScanError(rc, "ssm_layer_norm_bwd")
+    if io == rd:
+        g["dresidual"] = g["dx"]
     return g
 
 

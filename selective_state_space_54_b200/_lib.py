@@ -29,6 +29,7 @@ SSM_PATH_LOOKBACK_WS = 4
 SSM_FLAG_ZOH_EXACT = 1
 SSM_FLAG_SAVE_STATES = 2
 SSM_FLAG_TOKEN_MAJOR = 4
+SSM_FLAG_UNTIED = 8
 
 PATH_NAMES = {SSM_PATH_AUTO: "auto", SSM_PATH_LOOKBACK: "lookback",
               SSM_PATH_SPLIT_L: "split_l", SSM_PATH_PER_GROUP: "per_group",
@@ -41,6 +42,9 @@ EXPORTS = (
     "ssm_status_string", "ssm_scan_version", "ssm_scan_fwd_noalloc", "ssm_scan_step",
     "ssm_causal_conv1d", "ssm_causal_conv1d_bwd", "ssm_scan_test_fail_next",
     "ssm_scan_test_noalloc_reset_cycle",
+    "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step", "ssm_gated_scan_path",
+    "ssm_gated_scan_fwd_workspace_bytes", "ssm_gated_scan_bwd_workspace_bytes",
+    "ssm_layer_norm", "ssm_layer_norm_bwd", "ssm_layer_norm_bwd_workspace_bytes",
 )
 
 
@@ -85,6 +89,25 @@ def load(path: str | None = None):
     lib.ssm_causal_conv1d_bwd.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, vp, ci, vp, vp, vp, vp,
                                           vp, vp]
     lib.ssm_causal_conv1d_bwd.restype = ci
+    lib.ssm_gated_scan_fwd_workspace_bytes.argtypes = [shp]
+    lib.ssm_gated_scan_fwd_workspace_bytes.restype = sz
+    lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [shp]
+    lib.ssm_gated_scan_bwd_workspace_bytes.restype = sz
+    lib.ssm_gated_scan_path.argtypes = [shp]
+    lib.ssm_gated_scan_path.restype = i32
+    lib.ssm_gated_scan_fwd.argtypes = [shp] + [vp] * 9 + [sz, vp]
+    lib.ssm_gated_scan_fwd.restype = ci
+    lib.ssm_gated_scan_bwd.argtypes = [shp] + [vp] * 15 + [sz, vp]
+    lib.ssm_gated_scan_bwd.restype = ci
+    lib.ssm_gated_scan_step.argtypes = [shp] + [vp] * 7
+    lib.ssm_gated_scan_step.restype = ci
+    f32 = ctypes.c_float
+    lib.ssm_layer_norm.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, f32, vp, vp, vp]
+    lib.ssm_layer_norm.restype = ci
+    lib.ssm_layer_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+    lib.ssm_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.ssm_layer_norm_bwd.argtypes = [i64, i64, i32, i32, vp, vp, f32] + [vp] * 7 + [sz, vp]
+    lib.ssm_layer_norm_bwd.restype = ci
     lib.ssm_scan_check.argtypes = [vp, vp]
     lib.ssm_scan_check.restype = ci
     lib.ssm_scan_test_wait_timeout.argtypes = [vp, sz, i64, vp]

@@ -7,9 +7,33 @@
 #include <atomic>
 
 #include "ssm_common.cuh"
+#include "ssm_layer.cuh"
 #include "ssm_scan.h"
 
 using namespace ssm;
+
+namespace ssm {
+
+// Test hook (ssm_scan_test_fail_next): the number of upcoming entry-point
+// calls that report a launch failure instead of launching.
+static std::atomic<int32_t> g_fail_next{0};
+
+// Consumes one armed failure: cudaErrorLaunchFailure in place of the call's
+// first launch (nothing is launched), else cudaSuccess.
+cudaError_t injected_failure() {
+  int32_t v = g_fail_next.load();
+  while (v > 0 && !g_fail_next.compare_exchange_weak(v, v - 1)) {
+  }
+  return v > 0 ? cudaErrorLaunchFailure : cudaSuccess;
+}
+
+ssm_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return SSM_OK;
+  fprintf(stderr, "ssm_scan: CUDA error %s\n", cudaGetErrorString(e));
+  return SSM_ERR_CUDA;
+}
+
+}  // namespace ssm
 
 namespace {
 
@@ -223,25 +247,6 @@ ssm_status make_fwd_plan(const ssm_shape *s, FwdPlan *pl) {
   }
   *pl = p;
   return SSM_OK;
-}
-
-// Test hook (ssm_scan_test_fail_next): the number of upcoming entry-point
-// calls that report a launch failure instead of launching.
-std::atomic<int32_t> g_fail_next{0};
-
-// Consumes one armed failure: cudaErrorLaunchFailure in place of the call's
-// first launch (nothing is launched), else cudaSuccess.
-cudaError_t injected_failure() {
-  int32_t v = g_fail_next.load();
-  while (v > 0 && !g_fail_next.compare_exchange_weak(v, v - 1)) {
-  }
-  return v > 0 ? cudaErrorLaunchFailure : cudaSuccess;
-}
-
-ssm_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return SSM_OK;
-  fprintf(stderr, "ssm_scan: CUDA error %s\n", cudaGetErrorString(e));
-  return SSM_ERR_CUDA;
 }
 
 // Backward workspace: header, saved states (when the backward computes its
