@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssmscan.so")
 SOURCES = ["ssm_api.cu", "ssm_fwd.cu", "ssm_bwd.cu", "ssm_bwd16.cu", "ssm_noalloc.cu", "ssm_step.cu", "ssm_conv.cu",
-           "ssm_gscan.cu", "ssm_norm.cu", "ssm_layer_api.cu"]
+           "ssm_gscan.cu", "ssm_gscan_rows.cu", "ssm_gscan_tok.cu", "ssm_norm.cu", "ssm_layer_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -1,0 +1,182 @@
+// Device code shared by the gated recurrence's kernels (ssm_gscan_rows.cu,
+// ssm_gscan_tok.cu, ssm_gscan.cu).  Not part of the public interface.
+//
+//   g_t = sigmoid(-(f_t + bias)),  a_t = 1 - g_t
+//   h_t = a_t h_{t-1} + g_t u_t   (untied: + u_t),  h_{t-1} := 0 at a start
+//   y_t = h_t SiLU(z_t)
+// Backward, with d_t = dout_t SiLU(z_t) and P_t = a_t G_t (0 at a start):
+//   G_t = d_t + P_{t+1},  du = g G (untied: G),  dz = dout h SiLU'(z),
+//   df = G (h_{t-1} - u) a g   (untied: G h_{t-1} a g),  dh0 = P_0.
+//
+// A run of steps acts on the state entering it as h -> A h + B, and on the
+// gradient entering it from behind as P -> A P + R, with the same A = prod a_t.
+// A lane walks its own steps from zero for its run, the runs before it are
+// joined, and it walks its steps again from the state that enters them.
+//
+// A gate close to 1 (a memory of 1e5 steps) must not lose its 1 - a = g to the
+// rounding of a, nor a run its 1 - A: a_t is never formed on the way (h and P move
+// by x - g x in one rounding), and a run carries A and N = A - 1 side by side,
+// each built without cancellation:
+//   one step     A <- A - g A,   N <- N - g A
+//   two runs     A = A1 A2,      N = N1 + A1 N2
+// and is applied as x + N x + B while A > 1/2 and as A x + B below.  With A alone,
+// rounded at every step, 1e5 steps of a constant a = 1 - 1e-5 came out 2e-4 off.
+#pragma once
+
+#include "ssm_layer.cuh"
+
+namespace ssm {
+
+struct Run {
+  float A, N, B;
+};
+
+// The run applied to x.  With packed sequences (ST) a run that holds a start has A = 0
+// exactly and what came before counts for nothing, infinities and NaN included; a run
+// whose gates alone round to A = 0 is treated the same.
+template <bool ST>
+__device__ __forceinline__ float run_on(const Run &r, float x) {
+  const float far = fmaf(r.A, x, r.B), near = fmaf(r.N, x, x) + r.B;
+  const float v = r.N > -0.5f ? near : far;
+  if constexpr (ST) return r.A == 0.f ? r.B : v;
+  return v;
+}
+
+// Two runs joined, `own` the one on the side the result comes out of: a start in it
+// stays a start, whatever the other run holds.
+template <bool ST>
+__device__ __forceinline__ Run join(const Run &own, const Run &other) {
+  Run r;
+  r.B = run_on<ST>(own, other.B);
+  r.A = own.A * other.A;
+  r.N = fmaf(other.A, own.N, other.N);
+  if constexpr (ST) {
+    if (own.A == 0.f) {
+      r.A = 0.f;
+      r.N = -1.f;
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ Run no_run() { return Run{1.f, 0.f, 0.f}; }
+
+// one half of a pair zeroed where its bit says that a sequence starts
+__device__ __forceinline__ f2 zero_at(f2 v, bool lo, bool hi) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(lo ? 0.f : a, hi ? 0.f : b);
+}
+
+__device__ __forceinline__ f2 put_at(f2 v, bool lo, bool hi, float x) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(lo ? x : a, hi ? x : b);
+}
+
+// min(x, y) that lets a NaN in x pass
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// -g = -1 / (1 + e^f) on a pair; b2 is bias * log2(e).  e^f = inf gives -0.
+__device__ __forceinline__ f2 neg_gate2(f2 f, f2 b2) {
+  float x, y, d0, d1;
+  unpack2(fma2(f, splat2(kLog2e), b2), x, y);
+  unpack2(fma2(pack2(ex2(x), ex2(y)), splat2(-1.f), splat2(-1.f)), d0, d1);
+  return pack2(rcp_approx(d0), rcp_approx(d1));
+}
+
+// a g = e^f / (1 + e^f)^2 on a pair, from f and -g.  The exponent is held below
+// 2^120 (a is 1 to every bit from 2^24 on) so that inf * 0 does not arise.
+__device__ __forceinline__ f2 gate_slope2(f2 f, f2 b2, f2 ng) {
+  float x, y;
+  unpack2(fma2(f, splat2(kLog2e), b2), x, y);
+  const f2 e = pack2(ex2(min_nan(x, 120.f)), ex2(min_nan(y, 120.f)));
+  return mul2(mul2(e, ng), ng);
+}
+
+// 1 / (1 + e^-z) on a pair
+__device__ __forceinline__ f2 sigmoid2(f2 z) {
+  float x, y, d0, d1;
+  unpack2(mul2(z, splat2(-kLog2e)), x, y);
+  unpack2(add2(pack2(ex2(x), ex2(y)), splat2(1.f)), d0, d1);
+  return pack2(rcp_approx(d0), rcp_approx(d1));
+}
+
+// one step of the state: h - g (h - u), or h - g h + u
+template <bool TIED>
+__device__ __forceinline__ f2 state_step(f2 h, f2 ng, f2 u) {
+  if constexpr (TIED) return fma2(ng, fma2(u, splat2(-1.f), h), h);
+  return add2(fma2(ng, h, h), u);
+}
+
+// ---- what tiles hand on to one another ----------------------------------------
+// A word of the workspace is 0 until its value is there: values are stored with
+// every bit inverted, and the one pattern that would invert to 0 (a NaN) is
+// replaced by another NaN.  A word is written and read whole, so no fence is
+// needed: the value is its own flag.
+__device__ __forceinline__ unsigned as_word(float v) {
+  const unsigned b = __float_as_uint(v);
+  return b == 0xffffffffu ? 0x80000000u /* ~0x7fffffff, a NaN */ : ~b;
+}
+__device__ __forceinline__ float of_word(unsigned w) { return __uint_as_float(~w); }
+// A run as 64 bits: B, and N (> -1/2) or else A as a number without a sign.
+__device__ __forceinline__ void put_run(unsigned long long *p, const Run &r) {
+  const float e = r.N > -0.5f ? -fabsf(r.N) : fabsf(r.A);
+  const unsigned long long v = ((unsigned long long)as_word(r.B) << 32) | as_word(e);
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ Run of_words(unsigned long long v) {
+  Run r;
+  const float e = of_word((unsigned)v);
+  r.B = of_word((unsigned)(v >> 32));
+  const bool n = (__float_as_uint(e) >> 31) != 0u;
+  r.N = n ? e : e - 1.f;
+  r.A = n ? 1.f + e : e;
+  return r;
+}
+__device__ __forceinline__ void put_state(unsigned *p, float h) {
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(as_word(h)) : "memory");
+}
+__device__ __forceinline__ unsigned long long look64(const unsigned long long *p) {
+  unsigned long long v;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned look32(const unsigned *p) {
+  unsigned v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// The bounded wait for such words: spun(started, n, err) is false once
+// kWaitLimitNs have passed or another wait of the call has given up; the error
+// word is set then, and the caller goes on with what it has.
+__device__ __forceinline__ bool spun(unsigned long long &started, unsigned &n, unsigned *err) {
+  if (n++ == 0) {
+    started = global_ns();
+    return true;
+  }
+  __nanosleep(20);
+  if ((n & 63u) != 0) return true;
+  if (look32(err) != 0u) return false;
+  if (global_ns() - started > kWaitLimitNs) {
+    atomicOr(err, kErrWaitTimeout);
+    return false;
+  }
+  return true;
+}
+
+// Tile order.  Tiles are taken by ticket, the tiles of one time index before
+// those of the next, so a tile that is waited for was taken earlier and is
+// running or done.
+__device__ __forceinline__ unsigned take_ticket(unsigned *counter, unsigned *slot) {
+  if (threadIdx.x == 0) *slot = atomicAdd(counter, 1u);
+  __syncthreads();
+  return *slot;
+}
+
+}  // namespace ssm

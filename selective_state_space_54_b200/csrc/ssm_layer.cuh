@@ -12,10 +12,24 @@ namespace ssm {
 cudaError_t injected_failure();
 ssm_status cuda_status(cudaError_t e);
 
-// Gated recurrence: steps between two saved states, the state entering every
-// kGsCkpt-step chunk laid out [batch][chunk][dim] fp32.
-constexpr int kGsCkpt = 64;
-__host__ __device__ __forceinline__ int64_t gs_chunks(int64_t L) { return (L + kGsCkpt - 1) / kGsCkpt; }
+// Gated recurrence, channel-major: a lane takes 32 bytes of each tensor (16
+// bf16 or 8 fp32 steps), a warp 32 lanes of it; the state entering every warp's
+// run is what the backward starts from.  Saved [batch][dim][gs_row_chunks] fp32
+// (the first of a row is the initial state and is not read).
+constexpr int kGsLaneBytes = 32;
+__host__ __device__ __forceinline__ int gs_row_steps(int esize) { return 32 * kGsLaneBytes / esize; }
+__host__ __device__ __forceinline__ int64_t gs_row_chunks(int64_t L, int esize) {
+  return (L + gs_row_steps(esize) - 1) / gs_row_steps(esize);
+}
+constexpr int kGsTileWarps = 8;    // warps, and warp runs of steps, per look-back tile
+constexpr int kGsRowGroup = 32;    // tiles between two published states of a row
+// Token-major: a tile is kTokSteps steps of kTokChannels channels.  Saved
+// [batch][tile][dim] fp32, the state entering every tile.
+constexpr int kTokChannels = 64;
+constexpr int kTokSteps = 64;
+constexpr int kTokGroup = 16;      // tiles between two published states of a channel
+__host__ __device__ __forceinline__ int64_t gs_tok_tiles(int64_t L) { return (L + kTokSteps - 1) / kTokSteps; }
+__host__ __device__ __forceinline__ int64_t gs_tok_groups(int64_t dim) { return (dim + kTokChannels - 1) / kTokChannels; }
 
 struct GsParams {
   const void *u, *f, *z;             // [batch][dim][L] (or [batch][L][dim]) io dtype; z nullable
@@ -24,19 +38,33 @@ struct GsParams {
   const float *h0;                   // [batch][dim], nullable
   void *y;                           // as u; null: only the saved states are wanted
   float *last;                       // [batch][dim], nullable
-  float *ckpt;                       // [batch][gs_chunks(L)][dim], nullable (forward writes, backward reads)
+  float *ckpt;                       // saved states, nullable (forward writes, backward reads)
   int64_t batch, dim, L;
   int tok, untied;
+  int vec;                           // rows: 2 = 32-byte, 1 = 16-byte aligned, 0 = neither;
+                                     // token-major: channel pairs aligned
+  int start_vec;                     // starts rows 16-byte aligned
+  // look-back schedule (zeroed): error word, ticket counter, tile runs, group states
+  unsigned *err, *ticket;
+  unsigned long long *runs;
+  unsigned *states;
+  int64_t tiles;                     // time tiles per row or channel group
   // backward
   const void *dout;
   const float *dlast;                // [batch][dim], nullable
   void *du, *df, *dz;
-  float *dbias_part;                 // [batch][dim], nullable
+  float *dbias_part;                 // [part_rows][dim], nullable
+  int64_t part_rows;
   float *dbias;                      // [dim], nullable
   float *dh0;                        // [batch][dim], nullable
 };
-cudaError_t launch_gscan_fwd(int io_dtype, const GsParams &p, cudaStream_t s);
-cudaError_t launch_gscan_bwd(int io_dtype, const GsParams &p, cudaStream_t s);
+// path: SSM_PATH_PER_GROUP or SSM_PATH_LOOKBACK
+cudaError_t launch_gscan_fwd(int io_dtype, int path, const GsParams &p, cudaStream_t s);
+cudaError_t launch_gscan_bwd(int io_dtype, int path, const GsParams &p, cudaStream_t s);
+cudaError_t launch_gs_rows_fwd(int io_dtype, int path, const GsParams &p, cudaStream_t s);
+cudaError_t launch_gs_rows_bwd(int io_dtype, int path, const GsParams &p, cudaStream_t s);
+cudaError_t launch_gs_tok_fwd(int io_dtype, const GsParams &p, cudaStream_t s);
+cudaError_t launch_gs_tok_bwd(int io_dtype, const GsParams &p, cudaStream_t s);
 
 struct GsStepParams {
   const void *u, *f, *z;             // [batch][dim]; z nullable

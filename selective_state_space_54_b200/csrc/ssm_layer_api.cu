@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "ssm_layer.cuh"
 
@@ -37,21 +38,92 @@ ssm_status check_gscan(const ssm_shape *s) {
   return SSM_OK;
 }
 
-// Workspace of the forward: header, saved states.  Of the backward: header,
-// saved states (its own), per-batch partial sums of df_bias.
-struct GsLayout {
-  size_t off_ckpt, off_part, total;
+// Schedule and workspace of a call: header (error word), saved states, then for the
+// look-back schedule the ticket counter, the tiles' runs and the groups' states (zeroed
+// before each launch), then the partial sums of df_bias.
+struct GsPlan {
+  int path = SSM_PATH_PER_GROUP;
+  int64_t tiles = 1, part_rows = 0;
+  size_t ckpt_bytes = 0;
+  size_t off_ctl = 0, off_runs = 0, off_states = 0, end_ctl = 0;  // look-back
+  size_t off_part = 0, total = 0;
 };
-GsLayout gs_layout(const ssm_shape *s, bool bwd) {
-  GsLayout l;
-  const size_t ckpt = sizeof(float) * (size_t)s->batch * (size_t)gs_chunks(s->seqlen) * (size_t)s->dim;
-  l.off_ckpt = kHeaderBytes;
-  l.off_part = l.off_ckpt;
-  if (bwd || (s->flags & SSM_FLAG_SAVE_STATES)) l.off_part = round_up(l.off_ckpt + ckpt, 256);
-  l.total = l.off_part;
-  if (bwd) l.total = round_up(l.off_part + sizeof(float) * (size_t)s->batch * (size_t)s->dim, 256);
-  if (!bwd && !(s->flags & SSM_FLAG_SAVE_STATES)) l.total = 0;
-  return l;
+
+// AUTO, channel-major: a warp per row needs enough rows to keep the memory system busy
+// (each holds two passes of its row in flight); with fewer, rows longer than one tile
+// are split into tiles.
+constexpr int64_t kRowsPerSm = 8;
+
+ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
+  GsPlan l;
+  const bool tok = (s->flags & SSM_FLAG_TOKEN_MAJOR) != 0;
+  const int es = (int)esize(s->io_dtype);
+  const int64_t rows = s->batch * s->dim, L = s->seqlen;
+  const int64_t row_tile = (int64_t)kGsTileWarps * gs_row_steps(es);
+  l.path = tok ? SSM_PATH_LOOKBACK : s->path;
+  if (l.path == SSM_PATH_AUTO) {
+    l.path = SSM_PATH_PER_GROUP;
+    if (L > row_tile) {
+      const int sms = device_sms();
+      if (sms <= 0) return SSM_ERR_CUDA;
+      if (rows < kRowsPerSm * sms) l.path = SSM_PATH_LOOKBACK;
+    }
+  }
+  const int64_t chains = tok ? s->batch * gs_tok_groups(s->dim) : rows;  // sequences of tiles
+  const int64_t width = tok ? kTokChannels : 1, group = tok ? kTokGroup : kGsRowGroup;
+  if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L) : (L + row_tile - 1) / row_tile;
+  if ((double)chains * (double)l.tiles > 2.0e9) return SSM_ERR_UNSUPPORTED;  // a grid dimension
+  l.part_rows = s->batch * (l.path == SSM_PATH_LOOKBACK ? l.tiles : 1);
+  const bool save = bwd || (s->flags & SSM_FLAG_SAVE_STATES);
+  if (save)
+    l.ckpt_bytes = round_up(sizeof(float) * (size_t)rows * (size_t)(tok ? gs_tok_tiles(L) : gs_row_chunks(L, es)), 256);
+  size_t at = kHeaderBytes + l.ckpt_bytes;
+  const bool handoff = l.path == SSM_PATH_LOOKBACK && !(tok && l.tiles == 1);
+  if (handoff) {
+    l.off_ctl = at;
+    l.off_runs = l.off_ctl + 256;
+    l.off_states = l.off_runs + sizeof(unsigned long long) * (size_t)chains * (size_t)l.tiles * width;
+    at = l.off_states + sizeof(unsigned) * (size_t)chains * (size_t)((l.tiles + group - 1) / group) * width;
+    l.end_ctl = at = round_up(at, 256);
+  }
+  if (bwd) {
+    l.off_part = at;
+    at = round_up(at + sizeof(float) * (size_t)l.part_rows * (size_t)s->dim, 256);
+  }
+  l.total = (save || handoff) ? at : 0;
+  *out = l;
+  return SSM_OK;
+}
+
+// The control words of a launch zeroed, and their places set.
+cudaError_t gs_control(GsParams &p, const GsPlan &l, char *ws, cudaStream_t s) {
+  p.tiles = l.tiles;
+  if (!ws) return cudaSuccess;
+  p.err = reinterpret_cast<unsigned *>(ws);
+  if (!l.end_ctl) return cudaMemsetAsync(ws, 0, sizeof(unsigned), s);
+  p.ticket = reinterpret_cast<unsigned *>(ws + l.off_ctl);
+  p.runs = reinterpret_cast<unsigned long long *>(ws + l.off_runs);
+  p.states = reinterpret_cast<unsigned *>(ws + l.off_states);
+  if (l.ckpt_bytes == 0) return cudaMemsetAsync(ws, 0, l.end_ctl, s);
+  const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(unsigned), s);
+  return e != cudaSuccess ? e : cudaMemsetAsync(ws + l.off_ctl, 0, l.end_ctl - l.off_ctl, s);
+}
+
+// Widest access every given pointer and row allows: 32 or 16 bytes (channel-major rows),
+// or pairs of channels (token-major).
+void gs_access(GsParams &p, size_t es, std::initializer_list<const void *> ptrs) {
+  auto all = [&](size_t a) {
+    for (const void *q : ptrs)
+      if (!aligned(q, a)) return false;
+    return true;
+  };
+  if (p.tok) {
+    p.vec = p.dim % 2 == 0 && all(2 * es);
+  } else {
+    const size_t row = (size_t)p.L * es;
+    p.vec = row % 32 == 0 && all(32) ? 2 : row % 16 == 0 && all(16) ? 1 : 0;
+  }
+  p.start_vec = p.starts && p.L % 4 == 0 && aligned(p.starts, 4);
 }
 
 void gs_fill(GsParams &p, const ssm_shape *s, const void *u, const void *f, const void *z, const float *bias,
@@ -67,20 +139,20 @@ void gs_fill(GsParams &p, const ssm_shape *s, const void *u, const void *f, cons
 
 extern "C" {
 
-size_t ssm_gated_scan_fwd_workspace_bytes(const ssm_shape *shape) {
+static size_t gs_workspace_bytes(const ssm_shape *shape, bool bwd) {
+  GsPlan l;
   if (check_gscan(shape) != SSM_OK || shape->batch * shape->dim == 0 || shape->seqlen == 0) return 0;
-  return gs_layout(shape, false).total;
+  return gs_plan(shape, bwd, &l) == SSM_OK ? l.total : 0;
 }
 
-size_t ssm_gated_scan_bwd_workspace_bytes(const ssm_shape *shape) {
-  if (check_gscan(shape) != SSM_OK || shape->batch * shape->dim == 0 || shape->seqlen == 0) return 0;
-  return gs_layout(shape, true).total;
-}
+size_t ssm_gated_scan_fwd_workspace_bytes(const ssm_shape *shape) { return gs_workspace_bytes(shape, false); }
+
+size_t ssm_gated_scan_bwd_workspace_bytes(const ssm_shape *shape) { return gs_workspace_bytes(shape, true); }
 
 int32_t ssm_gated_scan_path(const ssm_shape *shape) {
-  if (check_gscan(shape) != SSM_OK) return SSM_PATH_AUTO;
-  if (shape->path != SSM_PATH_AUTO) return shape->path;
-  return (shape->flags & SSM_FLAG_TOKEN_MAJOR) ? SSM_PATH_LOOKBACK : SSM_PATH_PER_GROUP;
+  GsPlan l;
+  if (check_gscan(shape) != SSM_OK || gs_plan(shape, false, &l) != SSM_OK) return SSM_PATH_AUTO;
+  return l.path;
 }
 
 ssm_status ssm_gated_scan_fwd(const ssm_shape *shape, const void *u, const void *f, const void *z,
@@ -104,16 +176,20 @@ ssm_status ssm_gated_scan_fwd(const ssm_shape *shape, const void *u, const void 
   if (!u || !f || !y || !aligned(u, es) || !aligned(f, es) || !aligned(z, es) || !aligned(y, es))
     return SSM_ERR_INVALID_ARG;
   if (y == u || y == f || y == z) return SSM_ERR_INVALID_ARG;
-  const GsLayout l = gs_layout(shape, false);
+  GsPlan l;
+  const ssm_status pst = gs_plan(shape, false, &l);
+  if (pst != SSM_OK) return pst;
   if (l.total && (!workspace || ws_bytes < l.total || !aligned(workspace, 256))) return SSM_ERR_WORKSPACE;
   GsParams p;
   gs_fill(p, shape, u, f, z, f_bias, starts, initial_state);
   p.y = y; p.last = last_state;
-  if (shape->flags & SSM_FLAG_SAVE_STATES)
-    p.ckpt = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.off_ckpt);
-  const cudaError_t inj = injected_failure();
-  if (inj != cudaSuccess) return cuda_status(inj);
-  return cuda_status(launch_gscan_fwd(shape->io_dtype, p, s));
+  gs_access(p, es, {u, f, z, y});
+  char *ws = l.total ? static_cast<char *>(workspace) : nullptr;
+  if (shape->flags & SSM_FLAG_SAVE_STATES) p.ckpt = reinterpret_cast<float *>(ws + kHeaderBytes);
+  cudaError_t e = injected_failure();
+  if (e == cudaSuccess) e = gs_control(p, l, ws, s);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_gscan_fwd(shape->io_dtype, l.path, p, s));
 }
 
 ssm_status ssm_gated_scan_bwd(const ssm_shape *shape, const void *u, const void *f, const void *z,
@@ -152,24 +228,33 @@ ssm_status ssm_gated_scan_bwd(const ssm_shape *shape, const void *u, const void 
     for (int j = 0; j < i; ++j)
       if (out[i] == out[j]) return SSM_ERR_INVALID_ARG;
   }
-  const GsLayout l = gs_layout(shape, true);
+  GsPlan l;
+  const ssm_status pst = gs_plan(shape, true, &l);
+  if (pst != SSM_OK) return pst;
   if (!workspace || ws_bytes < l.total || !aligned(workspace, 256)) return SSM_ERR_WORKSPACE;
   char *ws = static_cast<char *>(workspace);
   GsParams p;
   gs_fill(p, shape, u, f, z, f_bias, starts, initial_state);
-  const cudaError_t inj = injected_failure();
-  if (inj != cudaSuccess) return cuda_status(inj);
+  gs_access(p, es, {u, f, z, dout, du, df, dz});
+  cudaError_t e = injected_failure();
+  if (e == cudaSuccess) e = gs_control(p, l, ws, s);
+  if (e != cudaSuccess) return cuda_status(e);
   if (fwd_workspace) {
     p.ckpt = reinterpret_cast<float *>(const_cast<char *>(static_cast<const char *>(fwd_workspace)) + kHeaderBytes);
-  } else {  // the forward once more, for the saved states alone
-    p.ckpt = reinterpret_cast<float *>(ws + l.off_ckpt);
-    const cudaError_t e = launch_gscan_fwd(shape->io_dtype, p, s);
+  } else {  // the forward once more, for the saved states alone (z plays no part in them)
+    p.ckpt = reinterpret_cast<float *>(ws + kHeaderBytes);
+    GsParams q = p;
+    q.z = nullptr;
+    e = launch_gscan_fwd(shape->io_dtype, l.path, q, s);
+    // the control words once more; the error word keeps what the forward wrote
+    if (e == cudaSuccess && l.end_ctl) e = cudaMemsetAsync(ws + l.off_ctl, 0, l.end_ctl - l.off_ctl, s);
     if (e != cudaSuccess) return cuda_status(e);
   }
   p.dout = dout; p.dlast = dlast_state; p.du = du; p.df = df; p.dz = dz;
   p.dbias = df_bias; p.dh0 = dinitial_state;
+  p.part_rows = l.part_rows;
   if (df_bias) p.dbias_part = reinterpret_cast<float *>(ws + l.off_part);
-  return cuda_status(launch_gscan_bwd(shape->io_dtype, p, s));
+  return cuda_status(launch_gscan_bwd(shape->io_dtype, l.path, p, s));
 }
 
 ssm_status ssm_gated_scan_step(const ssm_shape *shape, const void *u, const void *f, const void *z,
