@@ -83,7 +83,7 @@ struct NormParams {
   int64_t rows, dim;
   float eps;
 };
-cudaError_t launch_norm(int io_dtype, int res_dtype, const NormParams &p, cudaStream_t s);
+cudaError_t launch_norm(int io_dtype, int res_dtype, const NormParams &p, int sms, cudaStream_t s);
 
 struct NormBwdParams {
   const void *s, *dy, *dres_out;     // residual dtype, io dtype, residual dtype (nullable)

@@ -306,7 +306,9 @@ ssm_status ssm_layer_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t r
   p.rows = rows; p.dim = dim; p.eps = eps;
   const cudaError_t inj = injected_failure();
   if (inj != cudaSuccess) return cuda_status(inj);
-  return cuda_status(launch_norm(io_dtype, residual ? residual_dtype : io_dtype, p,
+  const int sms = device_sms();
+  if (sms <= 0) return SSM_ERR_CUDA;
+  return cuda_status(launch_norm(io_dtype, residual ? residual_dtype : io_dtype, p, sms,
                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 

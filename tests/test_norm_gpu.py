@@ -148,7 +148,6 @@ def test_offset_buffers_and_guards(cuda_device, dtype, residual):
     import selective_state_space_54_b200 as ssm
     for dim in (64, 1021, 4096, 17000):
         c = Case(cuda_device, 7, dim, dtype, residual, 10)
-        want = c.check()
 
         def off(t):
             if t is None:
@@ -165,9 +164,13 @@ def test_offset_buffers_and_guards(cuda_device, dtype, residual):
         out = ssm.layer_norm(c.x, c.w, c.b, residual=c.res, y=y)
         s = c.x if c.res is None else out[1]
         g = ssm.layer_norm_bwd(s, c.w, c.b, c.dy, dresidual_out=c.dro, out={"dx": dx, "dweight": dw})
-        assert_close(to_f64(y), to_f64(want[0]), synth.F32 if dtype == synth.F32 else synth.BF16, "y")
-        assert_close(to_f64(g["dx"]), to_f64(want[2]["dx"]), dtype, "dx")
-        assert_close(to_f64(dw), to_f64(want[2]["dweight"]), synth.F32, "dweight")
+        # against the reference, not against the aligned call: two correctly rounded results
+        # may stand on either side of a rounding boundary, a whole step apart
+        n = lambda t: None if t is None else to_f64(t)
+        assert_close(n(y), layer.layer_norm(n(s), n(c.w), n(c.b)), dtype, "y")
+        ref = layer.layer_norm_bwd(n(s), n(c.w), n(c.dy), dresidual=n(c.dro))
+        assert_close(n(g["dx"]), ref["ds"], dtype, "dx")
+        assert_close(n(dw), ref["dweight"], synth.F32, "dweight")
         for v, flat in ((y, yf), (dx, dxf), (dw, dwf)):
             assert (flat[:65] == 7).all() and (flat[65 + v.numel():] == 7).all()
 
