@@ -5,11 +5,17 @@
 //   ds = r (w dy - mean(w dy) - q mean(w dy q)) + dresidual_out
 //   dw = sum over rows of dy q,  db = sum over rows of dy
 //
-// Memory bound: every value is read once and written once.  A row sits in the
-// registers of the 1 to 32 warps that share it, so the mean and then the centred
-// squares are formed from registers (two short reductions, no second read and no
-// difference of large sums).  w and b are read per row, from L1.  Rows wider than the
-// registers hold take loops over memory instead.
+// Memory bound: every value is read once and written once.  1 to 16 warps share a row;
+// blocks walk the rows, each thread always on the same columns.  Where rows allow 16-byte
+// (fp32: 32-byte) accesses a thread loads its columns of the next rows into registers while
+// it works on the current ones; the mean and then the centred squares are formed from
+// registers (two short reductions, no second read and no difference of large sums), on f32x2
+// pairs.  What bounds such a kernel next to HBM is the work per row that does not shrink with
+// the row's share of a thread: reductions, barriers, addresses, w and b.  So the forward takes
+// two rows at a time where the registers allow.  Measured and dropped: rows copied ahead by
+// cp.async (16-byte copies of fp32 rows read every sector twice: 170 against 136 us at
+// 16384 x 4096 on an fp32 residual), w and b read from L1 for every single row (L1 at 70 %).
+// Rows wider than 16384 take walks over memory.
 #include "ssm_layer.cuh"
 
 #include <algorithm>
@@ -18,21 +24,8 @@ namespace ssm {
 
 namespace {
 
-// VEC values at i: 16-byte accesses for 8, element accesses for 1
-template <typename T, int VEC>
-__device__ __forceinline__ void load_v(const T *p, int64_t i, float (&o)[VEC]) {
-  if constexpr (VEC == 1) {
-    o[0] = IO<T>::get(p, i);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p + i));
-    o[0] = bf16_lo(v.x); o[1] = bf16_hi(v.x); o[2] = bf16_lo(v.y); o[3] = bf16_hi(v.y);
-    o[4] = bf16_lo(v.z); o[5] = bf16_hi(v.z); o[6] = bf16_lo(v.w); o[7] = bf16_hi(v.w);
-  } else {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p + i)), b = __ldcs(reinterpret_cast<const float4 *>(p + i) + 1);
-    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-  }
-}
 // w and b: read by every row, kept in L1
+// VEC values at i: 16-byte accesses for 8, element accesses for 1
 template <int VEC>
 __device__ __forceinline__ void load_w(const float *p, int64_t i, float (&o)[VEC]) {
   if constexpr (VEC == 1) o[0] = __ldg(p + i);
@@ -77,100 +70,236 @@ __device__ __forceinline__ float stored(float v) {
   return v;
 }
 
-// Sums of K values over the wpr warps of a row, the same in every thread of the row and
-// in a fixed order.  `red` alternates between calls, so one barrier each is enough.
-template <int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], int wpr, float *red) {
+// Sums of K values over the wpr warps of a row, the same in every thread of the row and in
+// a fixed order.  Each row of the block has 16 slots a value, 0 where there is no warp; the
+// array alternates between calls, so one barrier each is enough.  Q: quarters of the 16 in use.
+struct alignas(16) RowSums {
+  float v[3][8 * 16];
+};
+__device__ __forceinline__ void clear(RowSums &r) {
+  for (int i = threadIdx.x; i < 3 * 8 * 16; i += blockDim.x) (&r.v[0][0])[i] = 0.f;
+}
+template <int K, int Q = 4>
+__device__ __forceinline__ void row_sums(float (&v)[K], int wpr, int group, RowSums &red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   }
   if (wpr == 1) return;
-  const int w = threadIdx.x >> 5, first = w & ~(wpr - 1);
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) red[32 * k + w] = v[k];
+    for (int k = 0; k < K; ++k) red.v[k][group * 16 + (threadIdx.x >> 5) - group * wpr] = v[k];
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int i = 0; i < wpr; ++i) {
+  for (int k = 0; k < K; ++k) {
+    v[k] = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += red[32 * k + first + i];
+    for (int i = 0; i < Q; ++i) {
+      const float4 q = *reinterpret_cast<const float4 *>(&red.v[k][group * 16 + 4 * i]);
+      v[k] += (q.x + q.y) + (q.z + q.w);
+    }
   }
 }
 
+// ---- 8 neighbouring values of a row ---------------------------------------------------
+template <typename T>
+struct Raw8 {
+  uint32_t w[8 * sizeof(T) / 4];
+};
+template <typename T>
+__device__ __forceinline__ void load8(Raw8<T> &r, const T *p) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+  } else {
+    asm volatile("ld.global.cs.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                   "=r"(r.w[7])
+                 : "l"(p));
+  }
+}
+template <typename T>
+__device__ __forceinline__ f2 pair_of(const Raw8<T> &r, int e) {
+  if constexpr (sizeof(T) == 2) return pack2(bf16_lo(r.w[e]), bf16_hi(r.w[e]));
+  else return pack2(__uint_as_float(r.w[2 * e]), __uint_as_float(r.w[2 * e + 1]));
+}
+template <typename T>
+__device__ __forceinline__ void put8(T *p, const f2 (&o)[4]) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) unpack2(o[k], v[2 * k], v[2 * k + 1]);
+  if constexpr (sizeof(T) == 2) {
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  } else {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  }
+}
+// 8 fp32 parameters as pairs
+__device__ __forceinline__ void get_w(const float *p, f2 (&o)[4]) {
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2 *>(p)), b = __ldg(reinterpret_cast<const ulonglong2 *>(p) + 1);
+  o[0] = a.x; o[1] = a.y; o[2] = b.x; o[3] = b.y;
+}
+__device__ __forceinline__ f2 stored_bf16(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  const uint32_t w = pack_bf16x2(a, b);
+  return pack2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ float both(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
+}
+
 // ---- forward ------------------------------------------------------------------------
-// NV pieces of VEC values per thread; a block holds blockDim / (32 wpr) rows.
-template <typename T, typename R, int VEC, int NV>
-__global__ void k_norm(NormParams p, int wpr) {
-  __shared__ float red[2][32];
-  const int tpr = 32 * wpr, rpb = blockDim.x / tpr, tid = threadIdx.x & (tpr - 1);
-  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-  const bool live = row < p.rows;  // the last block's spare threads only keep the barriers company
-  const int64_t base = row * p.dim;
+// NV pieces of 8 values per thread and row, RB rows at a time, wpr warps a row; a block
+// holds blockDim / (32 wpr) such groups.  Q as in row_sums; MAXT threads, MINB blocks an SM.
+template <typename T, typename R, bool RES, int NV, int RB, int Q, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr) {
+  __shared__ RowSums red[2];
+  const int tpr = 32 * wpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
   const int dim = (int)p.dim;
+  const float inv = 1.f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * groups * RB;
+  int64_t row = ((int64_t)blockIdx.x * groups + group) * RB;
+  Raw8<T> x[RB][NV];
+  Raw8<R> a[RES ? RB : 1][NV];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = (k * tpr + tid) * 8;
+        if (r + j < p.rows && i < dim) {
+          load8<T>(x[j][k], static_cast<const T *>(p.x) + (r + j) * p.dim + i);
+          if constexpr (RES) load8<R>(a[j][k], static_cast<const R *>(p.res) + (r + j) * p.dim + i);
+        }
+      }
+    }
+  };
+  load(row);
+  clear(red[0]);
+  clear(red[1]);
+  __syncthreads();
+  // every group of the block takes the same rounds (barriers in row_sums)
+  for (int64_t r0 = (int64_t)blockIdx.x * groups * RB; r0 < p.rows; r0 += step, row += step) {
+    f2 v[RB][NV][4];
+    float sum[RB], sq[RB];
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      f2 t = splat2(0.f);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = (k * tpr + tid) * 8;
+        if (row + j >= p.rows || i >= dim) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][k][e] = pair_of<T>(x[j][k], e);
+        if constexpr (RES) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[j][k][e] = add2(v[j][k][e], pair_of<R>(a[j][k], e));
+            if constexpr (sizeof(R) == 2) v[j][k][e] = stored_bf16(v[j][k][e]);
+          }
+          put8<R>(static_cast<R *>(p.res_out) + (row + j) * p.dim + i, v[j][k]);
+        }
+        t = add2(t, add2(add2(v[j][k][0], v[j][k][1]), add2(v[j][k][2], v[j][k][3])));
+      }
+      sum[j] = both(t);
+    }
+    load(row + step);
+    row_sums<RB, Q>(sum, wpr, group, red[0]);
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const f2 m = splat2(-sum[j] * inv);
+      f2 t = splat2(0.f);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (row + j >= p.rows || (k * tpr + tid) * 8 >= dim) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[j][k][e] = add2(v[j][k][e], m);
+          t = fma2(v[j][k][e], v[j][k][e], t);
+        }
+      }
+      sq[j] = both(t);
+    }
+    row_sums<RB, Q>(sq, wpr, group, red[1]);
+#pragma unroll
+    for (int j = 0; j < RB; ++j) sq[j] = rsqrtf(fmaf(sq[j], inv, p.eps));
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (k * tpr + tid) * 8;
+      if (i >= dim) continue;
+      f2 w[4], b[4];
+      get_w(p.w + i, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = splat2(0.f);
+      if (p.b) get_w(p.b + i, b);
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        if (row + j >= p.rows) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][k][e] = fma2(mul2(v[j][k][e], splat2(sq[j])), w[e], b[e]);
+        put8<T>(static_cast<T *>(p.y) + (row + j) * p.dim + i, v[j][k]);
+      }
+    }
+  }
+}
+
+// rows without 16-byte accesses: NV columns per thread, one row (or several) per block
+template <typename T, typename R, int NV>
+__global__ void __launch_bounds__(512, 1) k_norm(NormParams p, int wpr) {
+  __shared__ RowSums red[2];
+  const int tpr = 32 * wpr, rpb = blockDim.x / tpr, tid = threadIdx.x & (tpr - 1), dim = (int)p.dim;
+  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, base = row * p.dim;
+  const bool live = row < p.rows;  // the last block's spare threads only keep the barriers company
+  clear(red[0]);
+  clear(red[1]);
+  __syncthreads();
   const T *x = static_cast<const T *>(p.x) + base;
-  float v[NV][VEC];
-  float sum[1] = {0.f};
+  float v[NV], sum[1] = {0.f}, sq[1] = {0.f};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = (k * tpr + tid) * VEC;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[k][e] = 0.f;
-    if (live && i < dim) load_v<T, VEC>(x, i, v[k]);
+    const int i = k * tpr + tid;
+    v[k] = live && i < dim ? IO<T>::get(x, i) : 0.f;
   }
   if (p.res) {
     const R *res = static_cast<const R *>(p.res) + base;
-    R *ro = static_cast<R *>(p.res_out) + base;
-    float a[NV][VEC];
+    float a[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) a[k][e] = 0.f;
-      if (live && i < dim) load_v<R, VEC>(res, i, a[k]);
+      const int i = k * tpr + tid;
+      a[k] = live && i < dim ? IO<R>::get(res, i) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[k][e] = stored<R>(v[k][e] + a[k][e]);
-      if (live && i < dim) store_v<R, VEC>(ro, i, v[k]);
+      const int i = k * tpr + tid;
+      v[k] = stored<R>(v[k] + a[k]);
+      if (live && i < dim) IO<R>::store1(static_cast<R *>(p.res_out) + base, i, v[k]);
     }
   }
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) sum[0] += v[k][e];
-  }
-  row_sums<1>(sum, wpr, red[0]);
+  for (int k = 0; k < NV; ++k) sum[0] += v[k];
+  row_sums<1>(sum, wpr, threadIdx.x / tpr, red[0]);
   const float m = sum[0] / (float)dim;
-  float sq[1] = {0.f};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const bool in = (k * tpr + tid) * VEC < dim;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[k][e] -= m;
-      if (in) sq[0] = fmaf(v[k][e], v[k][e], sq[0]);
-    }
+    v[k] -= m;
+    if (k * tpr + tid < dim) sq[0] = fmaf(v[k], v[k], sq[0]);
   }
-  row_sums<1>(sq, wpr, red[1]);
+  row_sums<1>(sq, wpr, threadIdx.x / tpr, red[1]);
   if (!live) return;
   const float r = 1.f / sqrtf(sq[0] / (float)dim + p.eps);
   T *y = static_cast<T *>(p.y) + base;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = (k * tpr + tid) * VEC;
-    if (i >= dim) continue;
-    float w[VEC], b[VEC];
-    load_w<VEC>(p.w, i, w);
-    if (p.b) load_w<VEC>(p.b, i, b);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) w[e] = p.b ? fmaf(v[k][e] * r, w[e], b[e]) : v[k][e] * r * w[e];
-    store_v<T, VEC>(y, i, w);
+    const int i = k * tpr + tid;
+    if (i < dim) IO<T>::store1(y, i, p.b ? fmaf(v[k] * r, p.w[i], p.b[i]) : v[k] * r * p.w[i]);
   }
 }
 
@@ -179,13 +308,16 @@ constexpr int kWideThreads = 512;
 // rows wider than the registers: three walks over the row, the later ones from L2
 template <typename T, typename R, int VEC>
 __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormParams p) {
-  __shared__ float red[2][32];
+  __shared__ RowSums red[2];
   const int64_t base = (int64_t)blockIdx.x * p.dim;
   const T *x = static_cast<const T *>(p.x) + base;
   const R *res = static_cast<const R *>(p.res);
   R *ro = static_cast<R *>(p.res_out) + base;
   T *y = static_cast<T *>(p.y) + base;
   const int64_t i0 = (int64_t)threadIdx.x * VEC, step = (int64_t)kWideThreads * VEC;
+  clear(red[0]);
+  clear(red[1]);
+  __syncthreads();
   float sum[1] = {0.f}, sq[1] = {0.f}, v[VEC], a[VEC], w[VEC];
   for (int64_t i = i0; i < p.dim; i += step) {
     load_again<T, VEC>(x, i, v);
@@ -203,7 +335,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormParams p) {
     if (res) load_again<R, VEC>(ro, i, v);
     else load_again<T, VEC>(x, i, v);
   };
-  row_sums<1>(sum, kWideThreads / 32, red[0]);
+  row_sums<1>(sum, kWideThreads / 32, 0, red[0]);
   const float m = sum[0] / (float)p.dim;
   for (int64_t i = i0; i < p.dim; i += step) {
     at(i);
@@ -213,7 +345,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormParams p) {
       sq[0] = fmaf(c, c, sq[0]);
     }
   }
-  row_sums<1>(sq, kWideThreads / 32, red[1]);
+  row_sums<1>(sq, kWideThreads / 32, 0, red[1]);
   const float r = 1.f / sqrtf(sq[0] / (float)p.dim + p.eps);
   for (int64_t i = i0; i < p.dim; i += step) {
     at(i);
@@ -226,127 +358,204 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormParams p) {
 }
 
 // ---- backward -----------------------------------------------------------------------
-// Blocks walk the rows, wpr warps a row, each thread on the same
-// columns of every row, whose dw and db it sums in registers; the block's sums go to the
-// workspace and k_norm_sum adds them in a fixed order.  w dy is rounded once and the same
-// wherever it is used (no contraction into the sums): a row whose terms cancel, such as
-// one of a single column, cancels exactly.
-// WARPS per block: 8, or 16 for rows that 8 do not hold.
-template <typename T, typename R, int VEC, int NV, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VEC * NV <= (VEC == 8 ? 8 : 4) ? 3 : 2)
-    k_norm_bwd(NormBwdParams p, int wpr) {
-  constexpr int kBwdThreads = 32 * WARPS;
-  __shared__ float red[2][96];
-  __shared__ float acc[kBwdThreads][9];
-  const int tpr = 32 * wpr, rpb = kBwdThreads / tpr, tid = threadIdx.x & (tpr - 1);
+// Blocks walk the rows, wpr warps a row, each thread on the same columns of every row,
+// whose dw and db it sums in registers.  The block's sums go to the workspace and k_norm_sum adds them in a fixed order.  w dy is rounded once and the
+// same wherever it is used (no contraction into the sums): a row whose terms cancel, such
+// as one of a single column, cancels exactly.
+__device__ __forceinline__ void grad_terms(float c, float g, float w, float (&s3)[3]) {
+  const float wd = __fmul_rn(w, g);
+  s3[0] = fmaf(c, c, s3[0]);
+  s3[1] = fmaf(wd, c, s3[1]);
+  s3[2] += wd;
+}
+
+// the sums of a block's rows (rpb of them at a time) of one column each, to `out` by the
+// first row's threads
+__device__ __forceinline__ void block_part(float *acc, float v, int tpr, int rpb, float *out, bool in) {
+  if (rpb > 1) {
+    __syncthreads();
+    acc[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x >= tpr) return;
+    v = 0.f;
+    for (int j = 0; j < rpb; ++j) v += acc[j * tpr + threadIdx.x];
+  }
+  if (in) *out = v;
+}
+
+template <typename T, typename R, bool DRO, int NV, int Q, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, int wpr) {
+  __shared__ RowSums red[2];
+  __shared__ float acc[MAXT];
+  const int tpr = 32 * wpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
   const int dim = (int)p.dim;
-  const float n = (float)dim;
-  float dw[NV][VEC], db[NV][VEC], w[NV][VEC];
+  const float inv = 1.f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  Raw8<R> s[NV];
+  Raw8<T> d[NV];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (k * tpr + tid) * 8;
+      if (r < p.rows && i < dim) {
+        load8<R>(s[k], static_cast<const R *>(p.s) + r * p.dim + i);
+        load8<T>(d[k], static_cast<const T *>(p.dy) + r * p.dim + i);
+      }
+    }
+  };
+  load(row);
+  f2 dw[NV][4], db[NV][4];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = (k * tpr + tid) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = w[k][e] = 0.f;
-    if (i < dim) load_w<VEC>(p.w, i, w[k]);
+    for (int e = 0; e < 4; ++e) dw[k][e] = db[k][e] = splat2(0.f);
   }
+  clear(red[0]);
+  clear(red[1]);
+  __syncthreads();
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, row += step) {
+    const bool live = row < p.rows;
+    f2 c[NV][4], t = splat2(0.f);
+    Raw8<T> g[NV];
+    Raw8<R> o[DRO ? NV : 1];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (k * tpr + tid) * 8;
+      if (!live || i >= dim) continue;
+      if constexpr (DRO) load8<R>(o[k], static_cast<const R *>(p.dres_out) + row * p.dim + i);
+      g[k] = d[k];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[k][e] = pair_of<R>(s[k], e);
+      t = add2(t, add2(add2(c[k][0], c[k][1]), add2(c[k][2], c[k][3])));
+    }
+    load(row + step);
+    float sum[1] = {both(t)};
+    row_sums<1, Q>(sum, wpr, group, red[0]);
+    const f2 m = splat2(-sum[0] * inv);
+    f2 a0 = splat2(0.f), a1 = splat2(0.f), a2 = splat2(0.f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (k * tpr + tid) * 8;
+      if (!live || i >= dim) continue;
+      f2 w[4];
+      get_w(p.w + i, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[k][e] = add2(c[k][e], m);
+        const f2 wd = mul2(w[e], pair_of<T>(g[k], e));
+        a0 = fma2(c[k][e], c[k][e], a0);
+        a1 = fma2(wd, c[k][e], a1);
+        a2 = add2(a2, wd);
+      }
+    }
+    float s3[3] = {both(a0), both(a1), both(a2)};
+    row_sums<3, Q>(s3, wpr, group, red[1]);
+    const float r = rsqrtf(fmaf(s3[0], inv, p.eps));
+    const f2 r2 = splat2(r), k1 = splat2(-(s3[1] * inv * r)), k2 = splat2(-(s3[2] * inv));
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (k * tpr + tid) * 8;
+      if (!live || i >= dim) continue;
+      f2 w[4], v[4];
+      get_w(p.w + i, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f2 q = mul2(c[k][e], r2), gd = pair_of<T>(g[k], e);
+        dw[k][e] = fma2(gd, q, dw[k][e]);
+        db[k][e] = add2(db[k][e], gd);
+        const f2 ds = fma2(q, k1, add2(mul2(w[e], gd), k2));
+        if constexpr (DRO) v[e] = fma2(r2, ds, pair_of<R>(o[k], e));
+        else v[e] = mul2(r2, ds);
+      }
+      put8<T>(static_cast<T *>(p.dx) + row * p.dim + i, v);
+      if constexpr (sizeof(R) != sizeof(T)) put8<R>(static_cast<R *>(p.dres) + row * p.dim + i, v);
+    }
+  }
+  float *part = p.part + (int64_t)blockIdx.x * 2 * p.dim;  // [block][2][dim]
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = (k * tpr + tid) * 8 + 2 * e;
+      float v[4];
+      unpack2(dw[k][e], v[0], v[1]);
+      unpack2(db[k][e], v[2], v[3]);
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        block_part(acc, v[h], tpr, groups, part + (h >> 1) * p.dim + i + (h & 1), i < dim);
+    }
+  }
+}
+
+// rows without 16-byte accesses: NV columns per thread, in registers
+template <typename T, typename R, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NV <= 4 ? 3 : 2) k_norm_bwd(NormBwdParams p, int wpr) {
+  __shared__ RowSums red[2];
+  __shared__ float acc[THREADS];
+  const int tpr = 32 * wpr, rpb = THREADS / tpr, tid = threadIdx.x & (tpr - 1), dim = (int)p.dim;
+  const float n = (float)dim;
+  float dw[NV], db[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) dw[k] = db[k] = 0.f;
+  clear(red[0]);
+  clear(red[1]);
+  __syncthreads();
   for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.rows; r0 += (int64_t)gridDim.x * rpb) {
     const int64_t row = r0 + threadIdx.x / tpr, base = row * p.dim;
     const bool live = row < p.rows;
-    float c[NV][VEC], g[NV][VEC], o[NV][VEC];
+    float c[NV], g[NV], sum[1] = {0.f}, s3[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c[k][e] = g[k][e] = o[k][e] = 0.f;
-      if (live && i < dim) {
-        load_v<R, VEC>(static_cast<const R *>(p.s) + base, i, c[k]);
-        load_v<T, VEC>(static_cast<const T *>(p.dy) + base, i, g[k]);
-      }
+      const int i = k * tpr + tid;
+      const bool in = live && i < dim;
+      c[k] = in ? IO<R>::get(static_cast<const R *>(p.s) + base, i) : 0.f;
+      g[k] = in ? IO<T>::get(static_cast<const T *>(p.dy) + base, i) : 0.f;
+      sum[0] += c[k];
     }
-    if (p.dres_out) {
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int i = (k * tpr + tid) * VEC;
-        if (live && i < dim) load_v<R, VEC>(static_cast<const R *>(p.dres_out) + base, i, o[k]);
-      }
-    }
-    float sum[1] = {0.f}, s3[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sum[0] += c[k][e];
-    }
-    row_sums<1>(sum, wpr, red[0]);
+    row_sums<1>(sum, wpr, threadIdx.x / tpr, red[0]);
     const float m = sum[0] / n;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if ((k * tpr + tid) * VEC < dim) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          c[k][e] -= m;
-          const float wd = __fmul_rn(w[k][e], g[k][e]);
-          s3[0] = fmaf(c[k][e], c[k][e], s3[0]);
-          s3[1] = fmaf(wd, c[k][e], s3[1]);
-          s3[2] += wd;
-        }
-      }
+      const int i = k * tpr + tid;
+      c[k] -= m;
+      if (i < dim) grad_terms(c[k], g[k], __ldg(p.w + i), s3);
     }
-    row_sums<3>(s3, wpr, red[1]);
+    row_sums<3>(s3, wpr, threadIdx.x / tpr, red[1]);
     const float r = 1.f / sqrtf(s3[0] / n + p.eps), k1 = s3[1] / n * r, k2 = s3[2] / n;
-    if (!live) continue;  // only in the last round: the barriers are behind
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * VEC;
-      if (i >= dim) continue;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float q = c[k][e] * r, wd = __fmul_rn(w[k][e], g[k][e]);
-        dw[k][e] = fmaf(g[k][e], q, dw[k][e]);
-        db[k][e] += g[k][e];
-        o[k][e] = fmaf(r, (wd - k2) - q * k1, o[k][e]);
-      }
-      store_v<T, VEC>(static_cast<T *>(p.dx) + base, i, o[k]);
-      if (p.dres) store_v<R, VEC>(static_cast<R *>(p.dres) + base, i, o[k]);
+      const int i = k * tpr + tid;
+      if (!live || i >= dim) continue;
+      const float q = c[k] * r, wd = __fmul_rn(__ldg(p.w + i), g[k]);
+      dw[k] = fmaf(g[k], q, dw[k]);
+      db[k] += g[k];
+      float o = p.dres_out ? IO<R>::get(static_cast<const R *>(p.dres_out) + base, i) : 0.f;
+      o = fmaf(r, (wd - k2) - q * k1, o);
+      IO<T>::store1(static_cast<T *>(p.dx) + base, i, o);
+      if (p.dres) IO<R>::store1(static_cast<R *>(p.dres) + base, i, o);
     }
   }
-  // the block's rows' sums together, then out: [block][2][dim]
   float *part = p.part + (int64_t)blockIdx.x * 2 * p.dim;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = (k * tpr + tid) * VEC;
-      if (rpb > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[threadIdx.x][e] = h ? db[k][e] : dw[k][e];
-        __syncthreads();
-        if (threadIdx.x < tpr && i < dim) {
-          float t[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            t[e] = 0.f;
-            for (int j = 0; j < rpb; ++j) t[e] += acc[j * tpr + tid][e];
-          }
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) part[h * p.dim + i + e] = t[e];
-        }
-      } else if (i < dim) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) part[h * p.dim + i + e] = h ? db[k][e] : dw[k][e];
-      }
-    }
+    const int i = k * tpr + tid;
+    block_part(acc, dw[k], tpr, rpb, part + i, i < dim);
+    block_part(acc, db[k], tpr, rpb, part + p.dim + i, i < dim);
   }
 }
 
 // wide rows: ds by walks over the row (one block each), mean and r kept for the columns
 template <typename T, typename R, int VEC>
 __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdParams p, float2 *stats) {
-  __shared__ float red[2][96];
+  __shared__ RowSums red[2];
   const int64_t base = (int64_t)blockIdx.x * p.dim;
   const R *s = static_cast<const R *>(p.s) + base;
   const T *dy = static_cast<const T *>(p.dy) + base;
   const int64_t i0 = (int64_t)threadIdx.x * VEC, step = (int64_t)kWideThreads * VEC;
+  clear(red[0]);
+  clear(red[1]);
+  __syncthreads();
   const float n = (float)p.dim;
   float sum[1] = {0.f}, s3[3] = {0.f, 0.f, 0.f}, c[VEC], g[VEC], w[VEC], o[VEC];
   for (int64_t i = i0; i < p.dim; i += step) {
@@ -354,7 +563,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdParams p,
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sum[0] += c[e];
   }
-  row_sums<1>(sum, kWideThreads / 32, red[0]);
+  row_sums<1>(sum, kWideThreads / 32, 0, red[0]);
   const float m = sum[0] / n;
   for (int64_t i = i0; i < p.dim; i += step) {
     load_again<R, VEC>(s, i, c);
@@ -368,7 +577,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdParams p,
       s3[2] += wd;
     }
   }
-  row_sums<3>(s3, kWideThreads / 32, red[1]);
+  row_sums<3>(s3, kWideThreads / 32, 0, red[1]);
   const float r = 1.f / sqrtf(s3[0] / n + p.eps), k1 = s3[1] / n * r, k2 = s3[2] / n;
   if (threadIdx.x == 0) stats[blockIdx.x] = make_float2(m, r);
   for (int64_t i = i0; i < p.dim; i += step) {
@@ -435,67 +644,138 @@ __global__ void __launch_bounds__(1024) k_norm_sum(const float *part, float *dw,
 }
 
 // ---- launches -----------------------------------------------------------------------
+bool a32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kFwdValues = 32;  // values of a row a thread holds at most, forward
-constexpr int kBwdValues = 16;  // backward (beside as many dw, db and w)
-constexpr int kBwdWidest = 16 * 32 * kBwdValues;
+constexpr int kWidest = 16384;     // columns that 16 warps hold at 32 values a thread
+constexpr int kWidestPlain = 8192; // the same without 16-byte accesses, backward
 
-template <typename T, typename R, int VEC, int NV>
+// Warps a row and pieces of 8 values a thread: up to 2048 columns 1, 2 or 4 warps (blocks
+// of 8 warps hold several rows), above that a block a row, as many warps as 16 values a
+// thread need (32 above 8192 columns).
+struct RowShape {
+  int wpr, nv, threads;
+};
+RowShape row_shape(int64_t dim, int64_t rows, int sms) {
+  RowShape r;
+  if (dim <= 2048) {
+    r.wpr = dim <= 512 ? 1 : dim <= 1024 ? 2 : 4;
+    // few rows: twice the warps, 8 values a thread
+    if (dim > 256 && rows * r.wpr < 8 * (int64_t)sms) r.wpr *= 2;
+    r.nv = dim > 256 * r.wpr ? 2 : 1;
+    r.threads = 256;
+  } else {
+    r.nv = dim <= 4096 && rows < sms ? 1 : dim <= 8192 ? 2 : 4;
+    r.wpr = (int)((dim + 256 * r.nv - 1) / (256 * r.nv));
+    r.threads = 32 * r.wpr;
+  }
+  return r;
+}
+
+template <typename T, typename R, bool RES, int NV, int RB, int Q, int MAXT, int MINB>
+cudaError_t norm_rows(const NormParams &p, const RowShape &sh, int sms, cudaStream_t s) {
+  const int rows = RB * (sh.threads / (32 * sh.wpr));  // a block's at a time
+  const int64_t need = (p.rows + rows - 1) / rows, fit = (int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads);
+  k_norm_rows<T, R, RES, NV, RB, Q, MAXT, MINB><<<(unsigned)std::min(need, fit), sh.threads, 0, s>>>(p, sh.wpr);
+  return cudaGetLastError();
+}
+
+template <typename T, typename R, bool RES>
+cudaError_t norm_vec(const NormParams &p, int sms, cudaStream_t s) {
+  const RowShape sh = row_shape(p.dim, p.rows, sms);
+  // two rows at a time while the next rows' registers (4 a piece in bf16, 8 in fp32) allow
+  constexpr int BYTES = (int)sizeof(T) + (RES ? (int)sizeof(R) : 0);
+  constexpr int RB = BYTES <= 6 ? 2 : 1, MINB = BYTES <= 2 ? 3 : 2;
+  if (sh.nv == 1) {
+    if (sh.threads <= 256) return norm_rows<T, R, RES, 1, 1, 2, 256, 4>(p, sh, sms, s);
+    return norm_rows<T, R, RES, 1, 1, 4, 512, 2>(p, sh, sms, s);
+  }
+  if (sh.nv == 2) {
+    if (sh.threads <= 256) return norm_rows<T, R, RES, 2, RB, 2, 256, MINB>(p, sh, sms, s);
+    return norm_rows<T, R, RES, 2, 1, 4, 512, 1>(p, sh, sms, s);
+  }
+  return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, sh, sms, s);
+}
+
+template <typename T, typename R, int NV>
 cudaError_t norm_nv(const NormParams &p, int wpr, cudaStream_t s) {
   const int threads = std::max(128, 32 * wpr), rpb = threads / (32 * wpr);
-  k_norm<T, R, VEC, NV><<<(unsigned)((p.rows + rpb - 1) / rpb), threads, 0, s>>>(p, wpr);
+  k_norm<T, R, NV><<<(unsigned)((p.rows + rpb - 1) / rpb), threads, 0, s>>>(p, wpr);
   return cudaGetLastError();
 }
 
 template <typename T, typename R>
 cudaError_t norm_t(const NormParams &p, int sms, cudaStream_t s) {
-  const bool vec = p.dim % 8 == 0 && a16(p.x) && a16(p.res) && a16(p.y) && a16(p.res_out) && a16(p.w) && a16(p.b);
-  const int per = vec ? 8 : 1;
-  if (p.dim > 512 * kFwdValues) {
+  auto at = [](const void *q, size_t es) { return es == 4 ? a32(q) : a16(q); };  // 8 values
+  const bool vec = p.dim % 8 == 0 && at(p.x, sizeof(T)) && at(p.res, sizeof(R)) && at(p.y, sizeof(T)) &&
+                   at(p.res_out, sizeof(R)) && a16(p.w) && a16(p.b);
+  if (p.dim > kWidest) {
     if (vec) k_norm_wide<T, R, 8><<<(unsigned)p.rows, kWideThreads, 0, s>>>(p);
     else k_norm_wide<T, R, 1><<<(unsigned)p.rows, kWideThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  // the fewest warps a row that hold it; more while the rows leave the machine empty
+  if (vec) return p.res ? norm_vec<T, R, true>(p, sms, s) : norm_vec<T, R, false>(p, sms, s);
+  // the fewest warps a row that hold it at 32 values a thread; more while the rows leave
+  // the machine empty
   int wpr = 1;
-  while (wpr * 32 * kFwdValues < p.dim) wpr *= 2;
-  while (wpr < 16 && p.rows * wpr < 16 * sms && wpr * 32 * per < p.dim) wpr *= 2;
-  const int nv = (int)((p.dim + 32 * wpr * per - 1) / (32 * wpr * per));
-  if (vec) {
-    if (nv <= 1) return norm_nv<T, R, 8, 1>(p, wpr, s);
-    if (nv <= 2) return norm_nv<T, R, 8, 2>(p, wpr, s);
-    if (nv <= 3) return norm_nv<T, R, 8, 3>(p, wpr, s);
-    return norm_nv<T, R, 8, 4>(p, wpr, s);
-  }
-  if (nv <= 4) return norm_nv<T, R, 1, 4>(p, wpr, s);
-  if (nv <= 8) return norm_nv<T, R, 1, 8>(p, wpr, s);
-  if (nv <= 16) return norm_nv<T, R, 1, 16>(p, wpr, s);
-  return norm_nv<T, R, 1, 32>(p, wpr, s);
+  while (wpr * 32 * 32 < p.dim) wpr *= 2;
+  while (wpr < 16 && p.rows * wpr < 16 * sms && wpr * 32 < p.dim) wpr *= 2;
+  const int nv = (int)((p.dim + 32 * wpr - 1) / (32 * wpr));
+  if (nv <= 4) return norm_nv<T, R, 4>(p, wpr, s);
+  if (nv <= 8) return norm_nv<T, R, 8>(p, wpr, s);
+  if (nv <= 16) return norm_nv<T, R, 16>(p, wpr, s);
+  return norm_nv<T, R, 32>(p, wpr, s);
 }
 
 // blocks of the backward: enough to fill the machine, no more than there are rows
 int64_t bwd_blocks_for(int64_t rows, int sms) { return std::max<int64_t>(1, std::min<int64_t>(rows, 3 * (int64_t)sms)); }
 
-template <typename T, typename R, int VEC, int NV, int WARPS>
-cudaError_t norm_bwd_nv(const NormBwdParams &p, int wpr, int sms, cudaStream_t s) {
-  auto kern = k_norm_bwd<T, R, VEC, NV, WARPS>;
-  int occ = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 32 * WARPS, 0);
-  if (e != cudaSuccess) return e;
-  const int rpb = WARPS / wpr;
-  const int64_t fit = (int64_t)std::max(occ, 1) * sms, need = (p.rows + rpb - 1) / rpb;
-  const int64_t blocks = std::min(std::min(need, fit), bwd_blocks_for(p.rows, sms));
-  kern<<<(unsigned)blocks, 32 * WARPS, 0, s>>>(p, wpr);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+cudaError_t norm_parts(const NormBwdParams &p, int64_t blocks, cudaStream_t s) {
   k_norm_sum<<<(unsigned)(((p.db ? 2 : 1) * p.dim + 31) / 32), dim3(32, 32), 0, s>>>(p.part, p.dw, p.db, blocks, p.dim);
   return cudaGetLastError();
 }
 
+template <typename T, typename R, bool DRO, int NV, int Q, int MAXT, int MINB>
+cudaError_t bwd_rows(const NormBwdParams &p, const RowShape &sh, int sms, cudaStream_t s) {
+  const int groups = sh.threads / (32 * sh.wpr);
+  const int64_t fit = (int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads);
+  const int64_t blocks = std::min(std::min((p.rows + groups - 1) / groups, fit), bwd_blocks_for(p.rows, sms));
+  k_norm_bwd_rows<T, R, DRO, NV, Q, MAXT, MINB><<<(unsigned)blocks, sh.threads, 0, s>>>(p, sh.wpr);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : norm_parts(p, blocks, s);
+}
+
+template <typename T, typename R, bool DRO>
+cudaError_t bwd_vec(const NormBwdParams &p, int sms, cudaStream_t s) {
+  const RowShape sh = row_shape(p.dim, p.rows, sms);
+  if (sh.nv == 1) {
+    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, 3>(p, sh, sms, s);
+    return bwd_rows<T, R, DRO, 1, 4, 512, 1>(p, sh, sms, s);
+  }
+  if (sh.nv == 2) {
+    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 2, 2, 256, 2>(p, sh, sms, s);
+    return bwd_rows<T, R, DRO, 2, 4, 512, 1>(p, sh, sms, s);
+  }
+  return bwd_rows<T, R, DRO, 4, 4, 512, 1>(p, sh, sms, s);
+}
+
+template <typename T, typename R, int NV, int THREADS>
+cudaError_t bwd_plain(const NormBwdParams &p, int wpr, int sms, cudaStream_t s) {
+  const int rpb = THREADS / (32 * wpr);
+  const int64_t fit = (int64_t)sms * (THREADS > 256 ? 1 : NV <= 4 ? 3 : 2);
+  const int64_t blocks = std::min(std::min((p.rows + rpb - 1) / rpb, fit), bwd_blocks_for(p.rows, sms));
+  k_norm_bwd<T, R, NV, THREADS><<<(unsigned)blocks, THREADS, 0, s>>>(p, wpr);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : norm_parts(p, blocks, s);
+}
+
 template <typename T, typename R>
 cudaError_t norm_bwd_t(const NormBwdParams &p, int sms, cudaStream_t s) {
-  const bool vec = p.dim % 8 == 0 && a16(p.s) && a16(p.dy) && a16(p.dres_out) && a16(p.dx) && a16(p.dres) && a16(p.w);
-  if (p.dim > kBwdWidest) {
+  auto at = [](const void *q, size_t es) { return es == 4 ? a32(q) : a16(q); };  // 8 values
+  const bool vec = p.dim % 8 == 0 && at(p.s, sizeof(R)) && at(p.dy, sizeof(T)) && at(p.dres_out, sizeof(R)) &&
+                   at(p.dx, sizeof(T)) && at(p.dres, sizeof(R)) && a16(p.w);
+  if (vec && p.dim <= kWidest) return p.dres_out ? bwd_vec<T, R, true>(p, sms, s) : bwd_vec<T, R, false>(p, sms, s);
+  if (p.dim > kWidestPlain) {
     const int64_t splits = bwd_blocks_for((p.rows + 31) / 32, sms);
     float2 *stats = reinterpret_cast<float2 *>(p.part + splits * 2 * p.dim);
     if (vec) k_norm_bwd_wide<T, R, 8><<<(unsigned)p.rows, kWideThreads, 0, s>>>(p, stats);
@@ -503,19 +783,15 @@ cudaError_t norm_bwd_t(const NormBwdParams &p, int sms, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     k_norm_cols<T, R><<<dim3((unsigned)((p.dim + 255) / 256), (unsigned)splits), 256, 0, s>>>(p, stats);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_norm_sum<<<(unsigned)(((p.db ? 2 : 1) * p.dim + 31) / 32), dim3(32, 32), 0, s>>>(p.part, p.dw, p.db, splits, p.dim);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : norm_parts(p, splits, s);
   }
-  // 8 values a thread while 8 warps hold the row, then 16, then 16 warps
   int wpr = 1;
-  while (wpr < 8 && wpr * 256 < p.dim) wpr *= 2;
-  if (p.dim > 8 * 32 * kBwdValues)
-    return vec ? norm_bwd_nv<T, R, 8, 2, 16>(p, 16, sms, s) : norm_bwd_nv<T, R, 1, 16, 16>(p, 16, sms, s);
-  const bool two = wpr * 256 < p.dim;
-  if (vec) return two ? norm_bwd_nv<T, R, 8, 2, 8>(p, wpr, sms, s) : norm_bwd_nv<T, R, 8, 1, 8>(p, wpr, sms, s);
-  if (wpr * 128 >= p.dim) return norm_bwd_nv<T, R, 1, 4, 8>(p, wpr, sms, s);
-  return two ? norm_bwd_nv<T, R, 1, 16, 8>(p, wpr, sms, s) : norm_bwd_nv<T, R, 1, 8, 8>(p, wpr, sms, s);
+  while (wpr < 8 && wpr * 128 < p.dim) wpr *= 2;
+  if (p.dim <= 1024) return bwd_plain<T, R, 4, 256>(p, wpr, sms, s);
+  if (p.dim <= 2048) return bwd_plain<T, R, 8, 256>(p, 8, sms, s);
+  if (p.dim <= 4096) return bwd_plain<T, R, 16, 256>(p, 8, sms, s);
+  return bwd_plain<T, R, 16, 512>(p, 16, sms, s);
 }
 
 }  // namespace
@@ -526,7 +802,7 @@ cudaError_t launch_norm(int io_dtype, int res_dtype, const NormParams &p, int sm
 }
 
 size_t norm_bwd_part_floats(int64_t rows, int64_t dim, int sms) {
-  return (size_t)bwd_blocks_for(rows, sms) * 2 * (size_t)dim + (dim > kBwdWidest ? 2 * (size_t)rows : 0);
+  return (size_t)bwd_blocks_for(rows, sms) * 2 * (size_t)dim + (dim > kWidestPlain ? 2 * (size_t)rows : 0);
 }
 
 cudaError_t launch_norm_bwd(int io_dtype, int res_dtype, const NormBwdParams &p, int sms, cudaStream_t s) {
