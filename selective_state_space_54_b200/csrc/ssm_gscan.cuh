@@ -170,13 +170,36 @@ __device__ __forceinline__ bool spun(unsigned long long &started, unsigned &n, u
   return true;
 }
 
-// Tile order.  Tiles are taken by ticket, the tiles of one time index before
-// those of the next, so a tile that is waited for was taken earlier and is
-// running or done.
-__device__ __forceinline__ unsigned take_ticket(unsigned *counter, unsigned *slot) {
-  if (threadIdx.x == 0) *slot = atomicAdd(counter, 1u);
-  __syncthreads();
-  return *slot;
+// ---- copies ahead into shared memory ---------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {  // zeros where !in
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4u : 0u) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Tile order.  Blocks take tiles by ticket, the tiles of one time index before those of
+// the next, so a tile that is waited for was taken earlier and is running or done (a block
+// takes its next tile before it has finished the current one, and finishes them in order).
+// One thread splits the ticket into the tile's time index, its chain (a row, or the channel
+// group of a batch element), and that into the batch element and what is left, in 32 bits
+// (the host checks that they fit): four 64-bit divisions in every thread cost more than the
+// gates.
+struct Place {
+  unsigned time, chain, batch, rest;
+};
+__device__ __forceinline__ Place place_of(unsigned ticket, unsigned chains, unsigned per_batch) {
+  Place q;
+  q.time = ticket / chains;
+  q.chain = ticket - q.time * chains;
+  q.batch = q.chain / per_batch;
+  q.rest = q.chain - q.batch * per_batch;
+  return q;
 }
 
 }  // namespace ssm

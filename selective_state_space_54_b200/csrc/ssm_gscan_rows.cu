@@ -2,17 +2,20 @@
 // channel of one batch element) is contiguous in time.
 //
 // Memory bound: 2 bytes a value in bf16 for each of u, f, z, y (forward) and
-// u, f, z, dout, du, df, dz (backward), against about 13 and 30 instruction
-// slots and 4 and 5 special-function results a value.  A lane takes 32
-// contiguous bytes (one whole sector) of each tensor with one load, as pairs
-// (t, t + S/2) on which the gates, the two half runs and the output run as f32x2
-// operations; the 32 lanes' runs are joined by shuffles.
+// u, f, z, dout, du, df, dz (backward), against 4 and 5 special-function results a value.
+// A warp copies its next steps into shared memory ahead (cp.async: whole 16-byte pieces, or
+// 4-byte words or elements where rows are not aligned, always a contiguous run a warp), reads
+// 32 bytes a lane from there (a run of 16 bf16 or 8 fp32 steps), as pairs (t, t + S/2) on
+// which the gates, the two half runs and the output run as f32x2 operations; the 32 lanes'
+// runs are joined by shuffles.
 //
-// Two schedules.  k_rows_*: a warp walks its row, one 32-lane pass after
-// another, the state in a register; rows shorter than a pass share a warp.
-// k_tiles_*: few long rows; eight warps take a tile of eight passes, tiles of a
-// row hand their runs on through the workspace.
+// Two schedules.  k_rows_*: a warp walks its row, one 32-lane pass after another, the state
+// in a register; rows shorter than a pass share a warp.  k_tiles_*: few long rows; the eight
+// warps of a block take a tile of eight passes, the tiles of a row hand their runs on through
+// the workspace.
 #include "ssm_gscan.cuh"
+
+#include <algorithm>
 
 namespace ssm {
 
@@ -26,7 +29,6 @@ struct Geo {
   static constexpr int S = kGsLaneBytes / (int)sizeof(T);  // steps per lane
   static constexpr int H = S / 2;                          // pairs per lane
   static constexpr int PASS = 32 * S;                      // steps per warp run
-  static constexpr int W = kGsLaneBytes / 4;               // words of a lane's chunk
 };
 
 // value i of a lane's chunk
@@ -40,35 +42,73 @@ __device__ __forceinline__ f2 pair_at(const uint32_t *w, int q) {
   return pack2(at<T>(w, q), at<T>(w, q + Geo<T>::H));
 }
 
-// the lane's S steps from src, zeros from `rem` on (rem may be negative)
+// ---- a warp's piece of one tensor in shared memory: 32 chunks of 32 bytes -------------
+// The two 16-byte units of a chunk change places in every other group of four lanes, so that
+// eight lanes reading their first (or second) units meet eight different bank groups.
+constexpr int kSlot = 1024;
+__device__ __forceinline__ uint32_t unit_at(int lane, int h) { return 16 * (2 * lane + (h ^ ((lane >> 2) & 1))); }
+// byte offset of word w (0..7) of a lane's chunk
+__device__ __forceinline__ uint32_t word_at(int lane, int w) { return unit_at(lane, w >> 2) + 4 * (w & 3); }
+
+// Which lanes share the row: W of them from lane `base`, this one being number sl.
+struct Lanes {
+  int W, base, sl;
+};
+
+// Copies the row's steps [t, t + W * S) (those below L; zeros beyond) to the group's chunks.
+// mode 2: 16-byte pieces, 1: 4-byte words, 0: elements (not asynchronous).
 template <typename T>
-__device__ __forceinline__ void load_chunk(uint32_t (&w)[8], const T *src, int64_t rem, int vec) {
-  constexpr int S = Geo<T>::S;
-  if (vec == 2 && rem >= S) {
-    asm volatile("ld.global.cs.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(src));
-  } else if (vec && rem >= S) {
+__device__ __forceinline__ void fill_slot(unsigned char *slot, const T *row, int64_t t, int64_t L, int mode, const Lanes &g) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
+  const int n = (int)(L - t < g.W * Geo<T>::S ? L - t : g.W * Geo<T>::S);  // steps there are
+  const T *src = row + t;
+  if (mode == 2) {
+    constexpr int E = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(src) + v);
-      w[4 * v] = q.x; w[4 * v + 1] = q.y; w[4 * v + 2] = q.z; w[4 * v + 3] = q.w;
+    for (int j = 0; j < 2; ++j) {
+      const int u = j * g.W + g.sl;
+      const bool in = u * E < n;
+      copy16(s + unit_at(g.base + (u >> 1), u & 1), in ? src + u * E : row, in);
+    }
+  } else if (mode == 1) {
+    constexpr int E = 4 / (int)sizeof(T);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int w = j * g.W + g.sl;
+      const bool in = w * E < n;
+      copy4(s + word_at(g.base + (w >> 3), w & 7), in ? src + w * E : row, in);
     }
   } else {
+    constexpr int S = Geo<T>::S;
+    T v[S];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 0u;
+    for (int j = 0; j < S; ++j) {
+      const int e = j * g.W + g.sl;
+      v[j] = e < n ? src[e] : T(0);
+    }
 #pragma unroll
-    for (int e = 0; e < S; ++e)
-      if (e < rem) {
-        if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-        else w[e] = __float_as_uint(src[e]);
-      }
+    for (int j = 0; j < S; ++j) {
+      const int e = j * g.W + g.sl, l = e / S, k = e % S;
+      *reinterpret_cast<T *>(slot + word_at(g.base + l, k * (int)sizeof(T) / 4) + (k * (int)sizeof(T) & 3)) = v[j];
+    }
   }
 }
 
-// stores the lane's S steps, given as pairs
+// the lane's chunk
+__device__ __forceinline__ void get_chunk(uint32_t (&w)[8], const unsigned char *slot, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(slot + unit_at(lane, h));
+    w[4 * h] = q.x; w[4 * h + 1] = q.y; w[4 * h + 2] = q.z; w[4 * h + 3] = q.w;
+  }
+}
+
+// Stores the group's steps [t, t + W * S) below L from the lanes' pairs.  Unaligned rows go
+// through `slot` (whose chunks the lanes have read) so that the warp stores contiguous runs;
+// a row's steps are written by its own lanes only, `live` being the same in all of them.
 template <typename T>
-__device__ __forceinline__ void store_chunk(T *dst, int64_t rem, int vec, const f2 (&v)[Geo<T>::H]) {
+__device__ __forceinline__ void put_chunk(unsigned char *slot, T *row, int64_t t, int64_t L, int mode, bool v32,
+                                          const Lanes &g, const f2 (&v)[Geo<T>::H], bool live) {
   constexpr int S = Geo<T>::S, H = Geo<T>::H;
   float o[S];
 #pragma unroll
@@ -79,20 +119,40 @@ __device__ __forceinline__ void store_chunk(T *dst, int64_t rem, int vec, const 
     if constexpr (sizeof(T) == 2) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
     else w[i] = __float_as_uint(o[i]);
   }
-  if (vec == 2 && rem >= S) {
-    asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else if (vec && rem >= S) {
-    __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-    __stcs(reinterpret_cast<uint4 *>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  if (mode == 2) {
+    T *dst = row + t + g.sl * S;
+    const int64_t rem = live ? L - t - g.sl * S : 0;
+    if (v32 && rem >= S) {
+      asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+    } else {  // whole 16-byte pieces
+      if (rem > 0) __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+      if (rem > S / 2) __stcs(reinterpret_cast<uint4 *>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *reinterpret_cast<uint4 *>(slot + unit_at(g.base + g.sl, h)) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+  __syncwarp();
+  const int n = live ? (int)(L - t < g.W * S ? L - t : g.W * S) : 0;
+  T *dst = row + t;
+  if (mode == 1) {
+    constexpr int E = 4 / (int)sizeof(T);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = j * g.W + g.sl;
+      if (k * E < n)
+        __stcs(reinterpret_cast<uint32_t *>(dst + k * E), *reinterpret_cast<const uint32_t *>(slot + word_at(g.base + (k >> 3), k & 7)));
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < S; ++e)
-      if (e < rem) {
-        if constexpr (sizeof(T) == 2) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-        else dst[e] = __uint_as_float(w[e]);
-      }
+    for (int j = 0; j < S; ++j) {
+      const int e = j * g.W + g.sl, l = e / S, k = e % S;
+      if (e < n)
+        dst[e] = *reinterpret_cast<const T *>(slot + word_at(g.base + l, k * (int)sizeof(T) / 4) + (k * (int)sizeof(T) & 3));
+    }
   }
 }
 
@@ -116,24 +176,28 @@ __device__ __forceinline__ unsigned load_starts(const uint8_t *src, int64_t rem,
 }
 
 // ---- forward ----------------------------------------------------------------------
-template <typename T, bool Z, bool ST>
-struct FwdChunk {
-  uint32_t u[8], f[8], z[Z ? 8 : 1];
-  unsigned st;
-  __device__ __forceinline__ void load(const GsParams &p, int64_t row, int64_t b, int64_t t0) {
-    const int64_t rem = p.L - t0, at0 = row * p.L + t0;
-    load_chunk<T>(f, static_cast<const T *>(p.f) + at0, rem, p.vec);
-    load_chunk<T>(u, static_cast<const T *>(p.u) + at0, rem, p.vec);
-    if constexpr (Z) load_chunk<T>(z, static_cast<const T *>(p.z) + at0, rem, p.vec);
-    if constexpr (ST) st = load_starts<Geo<T>::S>(p.starts + b * p.L + t0, rem, p.start_vec);
-    else st = 0;
-  }
-};
+// Slots of one stage of a warp: f, u, z (forward), f, u, z, dout (backward).
+constexpr int kSlotF = 0, kSlotU = kSlot, kSlotZ = 2 * kSlot;
+template <bool Z, bool BWD>
+constexpr int kStage = kSlot * (2 + (Z ? 1 : 0) + (BWD ? 1 : 0));
+template <bool Z>
+constexpr int kSlotG = kSlot * (Z ? 3 : 2);
+
+template <typename T, bool Z, bool BWD>
+__device__ __forceinline__ void fill_stage(unsigned char *st, const GsParams &p, int64_t row, int64_t t, const Lanes &g) {
+  const int64_t at0 = row * p.L;
+  fill_slot<T>(st + kSlotF, static_cast<const T *>(p.f) + at0, t, p.L, p.vec, g);
+  fill_slot<T>(st + kSlotU, static_cast<const T *>(p.u) + at0, t, p.L, p.vec, g);
+  if constexpr (Z) fill_slot<T>(st + kSlotZ, static_cast<const T *>(p.z) + at0, t, p.L, p.vec, g);
+  if constexpr (BWD) fill_slot<T>(st + kSlotG<Z>, static_cast<const T *>(p.dout) + at0, t, p.L, p.vec, g);
+}
 
 // -g of the lane's steps; steps past the row's end leave the state alone (g = 0)
 template <typename T>
-__device__ __forceinline__ void lane_gates(f2 (&ng)[Geo<T>::H], const uint32_t *f, f2 b2, int64_t rem) {
+__device__ __forceinline__ void lane_gates(f2 (&ng)[Geo<T>::H], const unsigned char *st, int lane, f2 b2, int64_t rem) {
   constexpr int H = Geo<T>::H;
+  uint32_t f[8];
+  get_chunk(f, st + kSlotF, lane);
 #pragma unroll
   for (int q = 0; q < H; ++q) ng[q] = neg_gate2(pair_at<T>(f, q), b2);
   if (rem < Geo<T>::S) {
@@ -147,8 +211,10 @@ struct Halves {
   Run lo, hi;
 };
 template <typename T, bool TIED, bool ST>
-__device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const uint32_t *u, unsigned st) {
+__device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const unsigned char *stage, int lane, unsigned st) {
   constexpr int H = Geo<T>::H;
+  uint32_t u[8];
+  get_chunk(u, stage + kSlotU, lane);
   f2 A = splat2(1.f), N = splat2(0.f), B = splat2(0.f);
 #pragma unroll
   for (int q = 0; q < H; ++q) {
@@ -173,7 +239,9 @@ __device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const uint
 // including each lane's own
 template <bool ST>
 __device__ __forceinline__ void scan_up(Run &r, int sl, int W) {
-  for (int o = 1; o < W; o <<= 1) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o >= W) break;  // the same in every lane
     const Run q = {__shfl_up_sync(kAll, r.A, o, W), __shfl_up_sync(kAll, r.N, o, W), __shfl_up_sync(kAll, r.B, o, W)};
     if (sl >= o) r = join<ST>(r, q);
   }
@@ -181,7 +249,9 @@ __device__ __forceinline__ void scan_up(Run &r, int sl, int W) {
 // the same from behind: the runs of the lane and of all after it, for the gradient
 template <bool ST>
 __device__ __forceinline__ void scan_down(Run &r, int sl, int W) {
-  for (int o = 1; o < W; o <<= 1) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o >= W) break;  // the same in every lane
     const Run q = {__shfl_down_sync(kAll, r.A, o, W), __shfl_down_sync(kAll, r.N, o, W),
                    __shfl_down_sync(kAll, r.B, o, W)};
     if (sl + o < W) r = join<ST>(r, q);
@@ -197,164 +267,250 @@ __device__ __forceinline__ Run run_of(const Run &r, int lane, int W) {
   return {__shfl_sync(kAll, r.A, lane, W), __shfl_sync(kAll, r.N, lane, W), __shfl_sync(kAll, r.B, lane, W)};
 }
 
-// the lane's outputs from the state h entering its first half run
+// the lane's outputs from the state entering its first half run
 template <typename T, bool TIED, bool Z, bool ST>
-__device__ __forceinline__ void lane_out(const GsParams &p, int64_t row, int64_t t0, const FwdChunk<T, Z, ST> &c,
-                                         const f2 (&ng)[Geo<T>::H], float hin, const Run &lo) {
+__device__ __forceinline__ void lane_out(const GsParams &p, int64_t row, int64_t t, unsigned char *stage, const Lanes &g,
+                                         unsigned st, const f2 (&ng)[Geo<T>::H], float hin, const Run &lo, bool live) {
   constexpr int H = Geo<T>::H;
   if (!p.y) return;
+  const int lane = g.base + g.sl;
   f2 h = pack2(hin, run_on<ST>(lo, hin)), o[H];
+  uint32_t u[8], z[8];
+  get_chunk(u, stage + kSlotU, lane);
+  if constexpr (Z) get_chunk(z, stage + kSlotZ, lane);
 #pragma unroll
   for (int q = 0; q < H; ++q) {
-    if constexpr (ST) h = zero_at(h, (c.st >> q) & 1u, (c.st >> (q + H)) & 1u);
-    h = state_step<TIED>(h, ng[q], pair_at<T>(c.u, q));
+    if constexpr (ST) h = zero_at(h, (st >> q) & 1u, (st >> (q + H)) & 1u);
+    h = state_step<TIED>(h, ng[q], pair_at<T>(u, q));
     if constexpr (Z) {
-      const f2 z = pair_at<T>(c.z, q);
-      o[q] = mul2(h, mul2(z, sigmoid2(z)));
+      const f2 zv = pair_at<T>(z, q);
+      o[q] = mul2(h, mul2(zv, sigmoid2(zv)));
     } else {
       o[q] = h;
     }
   }
-  store_chunk<T>(static_cast<T *>(p.y) + row * p.L + t0, p.L - t0, p.vec, o);
+  put_chunk<T>(stage + kSlotU, static_cast<T *>(p.y) + row * p.L, t, p.L, p.vec, p.v32, g, o, live);
 }
 
-template <typename T, bool TIED, bool Z, bool ST>
-__global__ void __launch_bounds__(kRowThreads) k_rows_fwd(GsParams p, int W) {
+// A warp's rows: W lanes each
+__device__ __forceinline__ Lanes lanes_of(int W) {
+  const int lane = threadIdx.x & 31;
+  return {W, lane & ~(W - 1), lane & (W - 1)};
+}
+
+constexpr int kRowStages = 3;  // the pass worked on and two on their way
+
+// FULL: 32 lanes a row; otherwise short rows of one chunk a lane, `short_lanes` lanes each.
+template <typename T, bool TIED, bool Z, bool ST, bool FULL>
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 5 : 6) k_rows_fwd(GsParams p, int short_lanes) {
   using G = Geo<T>;
-  const int lane = threadIdx.x & 31, sl = lane & (W - 1);
+  const int W = FULL ? 32 : short_lanes;
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char *ring = smem + (threadIdx.x >> 5) * kRowStages * kStage<Z, false>;
+  const Lanes g = lanes_of(W);
+  const int lane = threadIdx.x & 31;
   const int64_t warp = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) >> 5;
   const int64_t rows = p.batch * p.dim;
   int64_t row = warp * (32 / W) + lane / W;
   if (warp * (32 / W) >= rows) return;  // whole warps leave together
   const bool live = row < rows;
   if (!live) row = rows - 1;            // idle lanes read the last row and write nothing
-  const int64_t b = row / p.dim, d = row - b * p.dim;
+  const unsigned b = (unsigned)row / (unsigned)p.dim, d = (unsigned)row - b * (unsigned)p.dim;  // the host checks that rows fit
+  const int64_t chunks = FULL ? gs_row_chunks(p.L, sizeof(T)) : 1;
+#pragma unroll
+  for (int j = 0; j < kRowStages - 1; ++j) {
+    if (j < chunks) fill_stage<T, Z, false>(ring + j * kStage<Z, false>, p, row, j * (int64_t)G::PASS, g);
+    copies_commit();
+  }
   const f2 b2 = splat2(p.bias ? p.bias[d] * kLog2e : 0.f);
   float carry = p.h0 ? p.h0[row] : 0.f;
-  const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
-  FwdChunk<T, Z, ST> c;
-  c.load(p, row, b, (int64_t)sl * G::S);
+  int at = 0, ahead = kRowStages - 1;
   for (int64_t k = 0; k < chunks; ++k) {
-    const int64_t t0 = k * G::PASS + (int64_t)sl * G::S, rem = p.L - t0;
-    FwdChunk<T, Z, ST> next;
-    if (k + 1 < chunks) next.load(p, row, b, t0 + G::PASS);
+    const int64_t t = k * G::PASS, t0 = t + (int64_t)g.sl * G::S, rem = p.L - t0;
+    unsigned char *stage = ring + at * kStage<Z, false>;
+    if (k + kRowStages - 1 < chunks)
+      fill_stage<T, Z, false>(ring + ahead * kStage<Z, false>, p, row, t + (kRowStages - 1) * (int64_t)G::PASS, g);
+    copies_commit();
+    unsigned st = 0;
+    if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, p.start_vec);
+    copies_wait<kRowStages - 1>();
+    __syncwarp();
     if (p.ckpt && k > 0 && lane == 0) p.ckpt[row * chunks + k] = carry;
     f2 ng[G::H];
-    lane_gates<T>(ng, c.f, b2, rem);
-    const Halves hv = lane_run<T, TIED, ST>(ng, c.u, c.st);
+    lane_gates<T>(ng, stage, lane, b2, rem);
+    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
     Run r = join<ST>(hv.hi, hv.lo);
-    scan_up<ST>(r, sl, W);
+    scan_up<ST>(r, g.sl, W);
     const Run before = run_above(r, W);
-    const float hin = sl == 0 ? carry : run_on<ST>(before, carry);
+    const float hin = g.sl == 0 ? carry : run_on<ST>(before, carry);
     carry = run_on<ST>(run_of(r, W - 1, W), carry);
-    if (live && rem > 0) lane_out<T, TIED, Z, ST>(p, row, t0, c, ng, hin, hv.lo);
-    if (k + 1 < chunks) c = next;
+    lane_out<T, TIED, Z, ST>(p, row, t, stage, g, st, ng, hin, hv.lo, live);
+    __syncwarp();  // every lane is done with the stage before it is filled again
+    at = at + 1 == kRowStages ? 0 : at + 1;
+    ahead = ahead + 1 == kRowStages ? 0 : ahead + 1;
   }
-  if (p.last && live && sl == 0) p.last[row] = carry;
+  if (p.last && live && g.sl == 0) p.last[row] = carry;
 }
 
 // ---- look-back over tiles of a row ---------------------------------------------------
 // Called by one warp of tile `c` of a row (time index; from behind in the backward)
-// with the tile's own run in every lane: publishes it, and returns the state entering the
-// tile.  The tiles of a group of kGsRowGroup are joined in the order of their index
-// whatever the order they finish in, starting from the state that the last tile of the
-// group before published; so the result does not depend on timing.
-template <bool ST>
-__device__ __forceinline__ float look_back(const GsParams &p, int64_t row, int64_t c, float first, const Run &tile) {
+// with the runs of the tile's warps: publishes the tile's run, and returns the state
+// entering it (with one tile a group the caller, which walks the warps' runs anyway,
+// publishes the state leaving it instead).  The tiles of a group of p.group are joined in the order of their index whatever
+// the order they finish in, starting from the state that the last tile of the group before
+// published; so the result does not depend on timing.  `w` holds what the lane saw of the
+// word it needs when it looked ahead (peek): lane i the run of the group's tile i, lane 31
+// (never a predecessor's) the state.
+__device__ __forceinline__ const void *look_at(const GsParams &p, int64_t row, unsigned c) {
   const int lane = threadIdx.x & 31;
-  const int64_t groups = (p.tiles + kGsRowGroup - 1) / kGsRowGroup, g = c / kGsRowGroup;
-  const int in = (int)(c - g * kGsRowGroup);
-  unsigned long long *runs = p.runs + row * p.tiles;
-  unsigned *states = p.states + row * groups;
-  const bool last_in_group = in == kGsRowGroup - 1;
-  if (lane == 0 && !last_in_group) put_run(runs + c, tile);
-  // lane i waits for the run of the group's tile i, lane 31 (never a predecessor's) for the state
-  unsigned long long w = 0ull, started = 0;
-  unsigned n = 0, v = 0u;
-  if (lane < in) {
-    while ((w = look64(runs + g * kGsRowGroup + lane)) == 0ull)
-      if (!spun(started, n, p.err)) break;
-  } else if (lane == 31 && g > 0) {
-    while ((v = look32(states + g - 1)) == 0u)
-      if (!spun(started, n, p.err)) break;
+  const unsigned g = c / p.group, in = c - g * p.group;
+  if (lane < in) return p.runs + row * p.tiles + g * p.group + lane;
+  if (lane == 31 && g > 0) return p.states + row * p.groups + g - 1;
+  return nullptr;
+}
+__device__ __forceinline__ unsigned long long peek(const void *q) {
+  if (!q) return 0ull;
+  return (threadIdx.x & 31) == 31 ? look32(static_cast<const unsigned *>(q))
+                                  : look64(static_cast<const unsigned long long *>(q));
+}
+template <bool ST, bool FROM_BEHIND>
+__device__ __forceinline__ float look_back(const GsParams &p, int64_t row, unsigned c, float first, const Run *runs,
+                                           const void *q, unsigned long long w) {
+  const int lane = threadIdx.x & 31;
+  const unsigned g = c / p.group, in = c - g * p.group;
+  const bool last_in_group = in == p.group - 1;
+  Run tile = no_run();
+  if (p.group > 1) {
+#pragma unroll
+    for (int i = 0; i < kGsTileWarps; ++i) tile = join<ST>(runs[FROM_BEHIND ? kGsTileWarps - 1 - i : i], tile);
+    if (lane == 0 && !last_in_group) put_run(p.runs + row * p.tiles + c, tile);
+  }
+  unsigned long long started = 0;
+  unsigned n = 0;
+  while (q && w == 0ull) {
+    w = peek(q);
+    if (w == 0ull && !spun(started, n, p.err)) break;
   }
   __syncwarp();
-  Run r = lane < in ? of_words(w) : no_run();
-  const float base = __shfl_sync(kAll, of_word(v), 31);
-  scan_up<ST>(r, lane, 32);
-  const float h = run_on<ST>(run_of(r, 31, 32), g > 0 ? base : first);
-  if (lane == 0 && last_in_group) put_state(states + g, run_on<ST>(tile, h));
+  const float base = __shfl_sync(kAll, of_word((unsigned)w), 31);
+  float h = g > 0 ? base : first;
+  if (in > 0) {
+    Run r = lane < in ? of_words(w) : no_run();
+    scan_up<ST>(r, lane, 32);
+    h = run_on<ST>(run_of(r, 31, 32), h);
+  }
+  if (lane == 0 && last_in_group && p.group > 1) put_state(p.states + row * p.groups + g, run_on<ST>(tile, h));
   return h;
 }
 
 constexpr int kTileThreads = 32 * kGsTileWarps;
 
+// A tile of a row: where, and its chunk of this warp
+struct TileShared {
+  unsigned next;
+  Place place;
+  Run run[kGsTileWarps];
+  float in[kGsTileWarps], db[kGsTileWarps];
+};
+
+// Blocks stay and take tile after tile: the next tile's ticket is drawn and its steps are on
+// their way while the current one waits for the state entering it.
 template <typename T, bool TIED, bool Z, bool ST>
-__global__ void __launch_bounds__(kTileThreads) k_tiles_fwd(GsParams p) {
+__global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
   using G = Geo<T>;
-  __shared__ unsigned slot;
-  __shared__ Run sr[kGsTileWarps];
-  __shared__ float sh[kGsTileWarps];
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ TileShared sm;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t rows = p.batch * p.dim;
-  const int64_t ticket = take_ticket(p.ticket, &slot);
-  const int64_t c = ticket / rows, row = ticket - c * rows;
-  const int64_t b = row / p.dim, d = row - b * p.dim;
-  const f2 b2 = splat2(p.bias ? p.bias[d] * kLog2e : 0.f);
-  const int64_t chunk = c * kGsTileWarps + w, t0 = chunk * G::PASS + (int64_t)lane * G::S, rem = p.L - t0;
-  FwdChunk<T, Z, ST> ch;
-  ch.load(p, row, b, t0);
-  f2 ng[G::H];
-  lane_gates<T>(ng, ch.f, b2, rem);
-  const Halves hv = lane_run<T, TIED, ST>(ng, ch.u, ch.st);
-  Run r = join<ST>(hv.hi, hv.lo);
-  scan_up<ST>(r, lane, 32);
-  const Run before = run_above(r, 32);
-  if (lane == 31) sr[w] = r;
-  __syncthreads();
-  if (w == 0) {
-    Run tile = sr[0];
-#pragma unroll
-    for (int i = 1; i < kGsTileWarps; ++i) tile = join<ST>(sr[i], tile);
-    float h = look_back<ST>(p, row, c, p.h0 ? p.h0[row] : 0.f, tile);
-#pragma unroll
-    for (int i = 0; i < kGsTileWarps; ++i) {
-      if (lane == 0) sh[i] = h;
-      h = run_on<ST>(sr[i], h);
-    }
-    if (lane == 0 && c == p.tiles - 1 && p.last) p.last[row] = h;
+  unsigned char *ring = smem + w * 2 * kStage<Z, false>;
+  const Lanes lanes = {32, 0, lane};
+  const unsigned chains = (unsigned)(p.batch * p.dim), total = chains * (unsigned)p.tiles;
+  const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
+  if (threadIdx.x == 0) {
+    sm.next = atomicAdd(p.ticket, 1u);
+    sm.place = place_of(sm.next, chains, (unsigned)p.dim);
   }
   __syncthreads();
-  const float hw = sh[w];
-  const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
-  if (p.ckpt && lane == 0 && chunk > 0 && chunk < chunks) p.ckpt[row * chunks + chunk] = hw;
-  if (rem > 0) lane_out<T, TIED, Z, ST>(p, row, t0, ch, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo);
+  if (sm.next >= total) return;
+  Place at = sm.place;
+  __syncthreads();  // before the next ticket takes its place
+  fill_stage<T, Z, false>(ring, p, at.chain, ((int64_t)at.time * kGsTileWarps + w) * G::PASS, lanes);
+  copies_commit();
+  for (int stg = 0;; stg ^= 1) {
+    const int64_t row = at.chain, chunk = (int64_t)at.time * kGsTileWarps + w, t = chunk * G::PASS;
+    const int64_t t0 = t + lane * G::S, rem = p.L - t0;
+    unsigned char *stage = ring + stg * kStage<Z, false>;
+    unsigned drawn = 0;
+    if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
+    const void *q = nullptr;
+    unsigned long long seen = 0;
+    if (w == 0) {
+      q = look_at(p, row, at.time);
+      seen = peek(q);
+    }
+    const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
+    unsigned st = 0;
+    if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
+    copies_wait<0>();
+    __syncwarp();
+    f2 ng[G::H];
+    lane_gates<T>(ng, stage, lane, b2, rem);
+    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
+    Run r = join<ST>(hv.hi, hv.lo);
+    scan_up<ST>(r, lane, 32);
+    const Run before = run_above(r, 32);
+    if (lane == 31) sm.run[w] = r;
+    if (threadIdx.x == 0) {
+      sm.next = drawn;
+      sm.place = place_of(drawn, chains, (unsigned)p.dim);
+    }
+    __syncthreads();
+    const unsigned next_ticket = sm.next;
+    const Place next = sm.place;
+    if (next_ticket < total)
+      fill_stage<T, Z, false>(ring + (stg ^ 1) * kStage<Z, false>, p, next.chain,
+                              ((int64_t)next.time * kGsTileWarps + w) * G::PASS, lanes);
+    copies_commit();
+    if (w == 0) {
+      float h = look_back<ST, false>(p, row, at.time, p.h0 ? p.h0[row] : 0.f, sm.run, q, seen);
+#pragma unroll
+      for (int i = 0; i < kGsTileWarps; ++i) {
+        if (lane == 0) sm.in[i] = h;
+        h = run_on<ST>(sm.run[i], h);
+      }
+      if (lane == 0 && p.group == 1) put_state(p.states + row * p.groups + at.time, h);
+      if (lane == 0 && at.time == p.tiles - 1 && p.last) p.last[row] = h;
+    }
+    __syncthreads();
+    const float hw = sm.in[w];
+    if (p.ckpt && lane == 0 && chunk > 0 && chunk < chunks) p.ckpt[row * chunks + chunk] = hw;
+    lane_out<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo, t < p.L);
+    __syncwarp();
+    if (next_ticket >= total) break;
+    at = next;
+  }
 }
 
 // ---- backward ---------------------------------------------------------------------------
 // Per lane: -g, d (the gradient reaching h directly) and, from a walk of the states, dz
 // (stored at once) and w = (h_{t-1} - u) a g (untied h_{t-1} a g), which leave
 // du = g G and df = G w to the walk of the gradient from behind.
-template <typename T, bool Z, bool ST>
-struct BwdChunk : FwdChunk<T, Z, ST> {
-  uint32_t g[8];
-  __device__ __forceinline__ void load(const GsParams &p, int64_t row, int64_t b, int64_t t0) {
-    FwdChunk<T, Z, ST>::load(p, row, b, t0);
-    load_chunk<T>(g, static_cast<const T *>(p.dout) + row * p.L + t0, p.L - t0, p.vec);
-  }
-};
 
 // d of the lane's steps, and the gradient's half runs from zero
 template <typename T, bool Z, bool ST>
-__device__ __forceinline__ f2 lane_grad_run(f2 (&dh)[Geo<T>::H], const BwdChunk<T, Z, ST> &c,
+__device__ __forceinline__ f2 lane_grad_run(f2 (&dh)[Geo<T>::H], const unsigned char *stage, int lane, unsigned st,
                                             const f2 (&ng)[Geo<T>::H]) {
   constexpr int H = Geo<T>::H;
+  {
+    uint32_t g[8], z[8];
+    get_chunk(g, stage + kSlotG<Z>, lane);
+    if constexpr (Z) get_chunk(z, stage + kSlotZ, lane);
 #pragma unroll
-  for (int q = 0; q < H; ++q) {
-    dh[q] = pair_at<T>(c.g, q);
-    if constexpr (Z) {
-      const f2 z = pair_at<T>(c.z, q);
-      dh[q] = mul2(dh[q], mul2(z, sigmoid2(z)));
+    for (int q = 0; q < H; ++q) {
+      dh[q] = pair_at<T>(g, q);
+      if constexpr (Z) {
+        const f2 zv = pair_at<T>(z, q);
+        dh[q] = mul2(dh[q], mul2(zv, sigmoid2(zv)));
+      }
     }
   }
   f2 R = splat2(0.f);
@@ -362,7 +518,7 @@ __device__ __forceinline__ f2 lane_grad_run(f2 (&dh)[Geo<T>::H], const BwdChunk<
   for (int q = H - 1; q >= 0; --q) {
     const f2 s = add2(dh[q], R);
     R = fma2(ng[q], s, s);
-    if constexpr (ST) R = zero_at(R, (c.st >> q) & 1u, (c.st >> (q + H)) & 1u);
+    if constexpr (ST) R = zero_at(R, (st >> q) & 1u, (st >> (q + H)) & 1u);
   }
   return R;
 }
@@ -377,29 +533,36 @@ __device__ __forceinline__ Halves grad_halves(const Halves &h, f2 R) {
 // The lane's gradients, from the state entering it (hin) and the gradient reaching its
 // last step from behind (pin); returns the sum of its df.
 template <typename T, bool TIED, bool Z, bool ST>
-__device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int64_t t0, const BwdChunk<T, Z, ST> &c,
-                                            const f2 (&ng)[Geo<T>::H], const f2 (&dh)[Geo<T>::H], f2 b2, float hin,
-                                            float pin, const Run &lo, const Run &ghi, bool write) {
+__device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int64_t t, unsigned char *stage,
+                                            const Lanes &l, unsigned st, const f2 (&ng)[Geo<T>::H],
+                                            const f2 (&dh)[Geo<T>::H], f2 b2, float hin, float pin, const Run &lo,
+                                            const Run &ghi, bool live) {
   constexpr int H = Geo<T>::H, S = Geo<T>::S;
-  const int64_t at0 = row * p.L + t0, rem = p.L - t0;
+  const int lane = l.base + l.sl;
+  const int64_t at0 = row * p.L, rem = p.L - t - l.sl * S;
   f2 wt[H];
   {
     f2 h = pack2(hin, run_on<ST>(lo, hin)), o[H];
+    uint32_t f[8], u[8], z[8], g[8];
+    get_chunk(f, stage + kSlotF, lane);
+    get_chunk(u, stage + kSlotU, lane);
+    if constexpr (Z) {
+      get_chunk(z, stage + kSlotZ, lane);
+      get_chunk(g, stage + kSlotG<Z>, lane);
+    }
 #pragma unroll
     for (int q = 0; q < H; ++q) {
-      if constexpr (ST) h = zero_at(h, (c.st >> q) & 1u, (c.st >> (q + H)) & 1u);
-      const f2 u = pair_at<T>(c.u, q), ag = gate_slope2(pair_at<T>(c.f, q), b2, ng[q]);
-      wt[q] = mul2(TIED ? fma2(u, splat2(-1.f), h) : h, ag);
-      h = state_step<TIED>(h, ng[q], u);
+      if constexpr (ST) h = zero_at(h, (st >> q) & 1u, (st >> (q + H)) & 1u);
+      const f2 uv = pair_at<T>(u, q), ag = gate_slope2(pair_at<T>(f, q), b2, ng[q]);
+      wt[q] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
+      h = state_step<TIED>(h, ng[q], uv);
       if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
-        const f2 z = pair_at<T>(c.z, q), s = sigmoid2(z);
-        const f2 k = fma2(z, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
-        o[q] = mul2(mul2(pair_at<T>(c.g, q), h), mul2(s, k));
+        const f2 zv = pair_at<T>(z, q), s = sigmoid2(zv);
+        const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
+        o[q] = mul2(mul2(pair_at<T>(g, q), h), mul2(s, k));
       }
     }
-    if constexpr (Z) {
-      if (write) store_chunk<T>(static_cast<T *>(p.dz) + at0, rem, p.vec, o);
-    }
+    if constexpr (Z) put_chunk<T>(stage + kSlotZ, static_cast<T *>(p.dz) + at0, t, p.L, p.vec, p.v32, l, o, live);
   }
   f2 P = pack2(run_on<ST>(ghi, pin), pin), du[H], sum = splat2(0.f);
 #pragma unroll
@@ -408,137 +571,194 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
     du[q] = TIED ? mul2(mul2(G, ng[q]), splat2(-1.f)) : G;
     wt[q] = mul2(G, wt[q]);
     P = fma2(ng[q], G, G);
-    if constexpr (ST) P = zero_at(P, (c.st >> q) & 1u, (c.st >> (q + H)) & 1u);
+    if constexpr (ST) P = zero_at(P, (st >> q) & 1u, (st >> (q + H)) & 1u);
   }
+  put_chunk<T>(stage + kSlotU, static_cast<T *>(p.du) + at0, t, p.L, p.vec, p.v32, l, du, live);
+  put_chunk<T>(stage + kSlotF, static_cast<T *>(p.df) + at0, t, p.L, p.vec, p.v32, l, wt, live);
   if (rem < S) {
 #pragma unroll
     for (int q = 0; q < H; ++q) wt[q] = zero_at(wt[q], q >= rem, q + H >= rem);
   }
 #pragma unroll
   for (int q = 0; q < H; ++q) sum = add2(sum, wt[q]);
-  if (write) {
-    store_chunk<T>(static_cast<T *>(p.du) + at0, rem, p.vec, du);
-    store_chunk<T>(static_cast<T *>(p.df) + at0, rem, p.vec, wt);
-  }
   float s0, s1;
   unpack2(sum, s0, s1);
   return s0 + s1;
 }
 
-template <typename T, bool TIED, bool Z, bool ST>
-__global__ void __launch_bounds__(kRowThreads, 4) k_rows_bwd(GsParams p, int W) {
+constexpr int kRowBwdStages = 2;
+
+template <typename T, bool TIED, bool Z, bool ST, bool FULL>
+__global__ void __launch_bounds__(kRowThreads, 4) k_rows_bwd(GsParams p, int short_lanes) {
   using G = Geo<T>;
-  const int lane = threadIdx.x & 31, sl = lane & (W - 1);
+  const int W = FULL ? 32 : short_lanes;
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char *ring = smem + (threadIdx.x >> 5) * kRowBwdStages * kStage<Z, true>;
+  const Lanes l = lanes_of(W);
+  const int lane = threadIdx.x & 31;
   const int64_t warp = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) >> 5;
   const int64_t rows = p.batch * p.dim;
   int64_t row = warp * (32 / W) + lane / W;
   if (warp * (32 / W) >= rows) return;
   const bool live = row < rows;
   if (!live) row = rows - 1;
-  const int64_t b = row / p.dim, d = row - b * p.dim;
+  const unsigned b = (unsigned)row / (unsigned)p.dim, d = (unsigned)row - b * (unsigned)p.dim;
+  const int64_t chunks = FULL ? gs_row_chunks(p.L, sizeof(T)) : 1;
+  fill_stage<T, Z, true>(ring, p, row, (chunks - 1) * (int64_t)G::PASS, l);
+  copies_commit();
   const f2 b2 = splat2(p.bias ? p.bias[d] * kLog2e : 0.f);
   float pc = p.dlast ? p.dlast[row] : 0.f, db = 0.f;
-  const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
-  for (int64_t k = chunks - 1; k >= 0; --k) {
-    const int64_t t0 = k * G::PASS + (int64_t)sl * G::S, rem = p.L - t0;
-    BwdChunk<T, Z, ST> c;
-    c.load(p, row, b, t0);
+  int at = 0;
+  for (int64_t k = chunks - 1; k >= 0; --k, at ^= 1) {
+    const int64_t t = k * G::PASS, t0 = t + (int64_t)l.sl * G::S, rem = p.L - t0;
+    unsigned char *stage = ring + at * kStage<Z, true>;
+    if (k > 0) fill_stage<T, Z, true>(ring + (at ^ 1) * kStage<Z, true>, p, row, t - G::PASS, l);
+    copies_commit();
     const float h0 = k > 0 ? p.ckpt[row * chunks + k] : (p.h0 ? p.h0[row] : 0.f);
+    unsigned st = 0;
+    if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, p.start_vec);
+    copies_wait<1>();
+    __syncwarp();
     f2 ng[G::H], dh[G::H];
-    lane_gates<T>(ng, c.f, b2, rem);
-    const Halves hv = lane_run<T, TIED, ST>(ng, c.u, c.st);
-    const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, c, ng));
+    lane_gates<T>(ng, stage, lane, b2, rem);
+    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
+    const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, stage, lane, st, ng));
     Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
-    scan_up<ST>(r, sl, W);
-    scan_down<ST>(g, sl, W);
+    scan_up<ST>(r, l.sl, W);
+    scan_down<ST>(g, l.sl, W);
     const Run before = run_above(r, W), after = run_below(g, W);
-    const float hin = sl == 0 ? h0 : run_on<ST>(before, h0);
-    const float pin = sl == W - 1 ? pc : run_on<ST>(after, pc);
+    const float hin = l.sl == 0 ? h0 : run_on<ST>(before, h0);
+    const float pin = l.sl == W - 1 ? pc : run_on<ST>(after, pc);
     pc = run_on<ST>(run_of(g, 0, W), pc);
-    db += lane_grads<T, TIED, Z, ST>(p, row, t0, c, ng, dh, b2, hin, pin, hv.lo, gv.hi, live && rem > 0);
+    db += lane_grads<T, TIED, Z, ST>(p, row, t, stage, l, st, ng, dh, b2, hin, pin, hv.lo, gv.hi, live);
+    __syncwarp();  // every lane is done with the stage before it is filled again
   }
-  if (p.dh0 && live && sl == 0) p.dh0[row] = pc;
+  if (p.dh0 && live && l.sl == 0) p.dh0[row] = pc;
   if (p.dbias_part) {
     for (int o = 1; o < W; o <<= 1) db += __shfl_xor_sync(kAll, db, o, W);
-    if (live && sl == 0) p.dbias_part[row] = db;
+    if (live && l.sl == 0) p.dbias_part[row] = db;
   }
 }
 
 template <typename T, bool TIED, bool Z, bool ST>
 __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
   using G = Geo<T>;
-  __shared__ unsigned slot;
-  __shared__ Run sr[kGsTileWarps];
-  __shared__ float sp[kGsTileWarps], sdb[kGsTileWarps];
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ TileShared sm;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t rows = p.batch * p.dim;
-  const int64_t ticket = take_ticket(p.ticket, &slot);
-  const int64_t cb = ticket / rows, row = ticket - cb * rows, c = p.tiles - 1 - cb;  // from behind
-  const int64_t b = row / p.dim, d = row - b * p.dim;
-  const f2 b2 = splat2(p.bias ? p.bias[d] * kLog2e : 0.f);
+  unsigned char *ring = smem + w * 2 * kStage<Z, true>;
+  const Lanes lanes = {32, 0, lane};
+  const unsigned chains = (unsigned)(p.batch * p.dim), total = chains * (unsigned)p.tiles;
   const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
-  const int64_t chunk = c * kGsTileWarps + w, t0 = chunk * G::PASS + (int64_t)lane * G::S, rem = p.L - t0;
-  BwdChunk<T, Z, ST> ch;
-  ch.load(p, row, b, t0);
-  const float h0 = chunk >= chunks ? 0.f : chunk > 0 ? p.ckpt[row * chunks + chunk] : (p.h0 ? p.h0[row] : 0.f);
-  f2 ng[G::H], dh[G::H];
-  lane_gates<T>(ng, ch.f, b2, rem);
-  const Halves hv = lane_run<T, TIED, ST>(ng, ch.u, ch.st);
-  const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, ch, ng));
-  Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
-  scan_up<ST>(r, lane, 32);
-  scan_down<ST>(g, lane, 32);
-  const Run before = run_above(r, 32), after = run_below(g, 32);
-  const float hin = lane == 0 ? h0 : run_on<ST>(before, h0);
-  if (lane == 0) sr[w] = g;
-  __syncthreads();
-  if (w == 0) {
-    Run tile = sr[kGsTileWarps - 1];
-#pragma unroll
-    for (int i = kGsTileWarps - 2; i >= 0; --i) tile = join<ST>(sr[i], tile);
-    float P = look_back<ST>(p, row, cb, p.dlast ? p.dlast[row] : 0.f, tile);
-#pragma unroll
-    for (int i = kGsTileWarps - 1; i >= 0; --i) {
-      if (lane == 0) sp[i] = P;
-      P = run_on<ST>(sr[i], P);
-    }
-    if (lane == 0 && c == 0 && p.dh0) p.dh0[row] = P;
+  // the warp's chunk of a tile taken from behind; a tile's chunks past the row's end are empty
+  auto chunk_of = [&](unsigned time) { return (int64_t)(p.tiles - 1 - time) * kGsTileWarps + w; };
+  if (threadIdx.x == 0) {
+    sm.next = atomicAdd(p.ticket, 1u);
+    sm.place = place_of(sm.next, chains, (unsigned)p.dim);
   }
   __syncthreads();
-  const float pw = sp[w];
-  float db = lane_grads<T, TIED, Z, ST>(p, row, t0, ch, ng, dh, b2, hin, lane == 31 ? pw : run_on<ST>(after, pw),
-                                        hv.lo, gv.hi, rem > 0);
-  if (p.dbias_part) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) db += __shfl_xor_sync(kAll, db, o);
-    if (lane == 0) sdb[w] = db;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float t = 0.f;
-#pragma unroll
-      for (int i = 0; i < kGsTileWarps; ++i) t += sdb[i];
-      p.dbias_part[(b * p.tiles + c) * p.dim + d] = t;
+  if (sm.next >= total) return;
+  Place at = sm.place;
+  __syncthreads();  // before the next ticket takes its place
+  fill_stage<T, Z, true>(ring, p, at.chain, chunk_of(at.time) * G::PASS, lanes);
+  copies_commit();
+  for (int stg = 0;; stg ^= 1) {
+    const int64_t row = at.chain, chunk = chunk_of(at.time), t = chunk * G::PASS;
+    const int64_t t0 = t + lane * G::S, rem = p.L - t0;
+    unsigned char *stage = ring + stg * kStage<Z, true>;
+    unsigned drawn = 0;
+    if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
+    const void *q = nullptr;
+    unsigned long long seen = 0;
+    if (w == 0) {
+      q = look_at(p, row, at.time);
+      seen = peek(q);
     }
+    const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
+    const float h0 = chunk >= chunks ? 0.f : chunk > 0 ? p.ckpt[row * chunks + chunk] : (p.h0 ? p.h0[row] : 0.f);
+    unsigned st = 0;
+    if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
+    copies_wait<0>();
+    __syncwarp();
+    f2 ng[G::H], dh[G::H];
+    lane_gates<T>(ng, stage, lane, b2, rem);
+    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
+    const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, stage, lane, st, ng));
+    Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
+    scan_up<ST>(r, lane, 32);
+    scan_down<ST>(g, lane, 32);
+    const Run before = run_above(r, 32), after = run_below(g, 32);
+    const float hin = lane == 0 ? h0 : run_on<ST>(before, h0);
+    if (lane == 0) sm.run[w] = g;
+    if (threadIdx.x == 0) {
+      sm.next = drawn;
+      sm.place = place_of(drawn, chains, (unsigned)p.dim);
+    }
+    __syncthreads();
+    const unsigned next_ticket = sm.next;
+    const Place next = sm.place;
+    if (next_ticket < total)
+      fill_stage<T, Z, true>(ring + (stg ^ 1) * kStage<Z, true>, p, next.chain, chunk_of(next.time) * G::PASS, lanes);
+    copies_commit();
+    if (w == 0) {
+      float P = look_back<ST, true>(p, row, at.time, p.dlast ? p.dlast[row] : 0.f, sm.run, q, seen);
+#pragma unroll
+      for (int i = kGsTileWarps - 1; i >= 0; --i) {
+        if (lane == 0) sm.in[i] = P;
+        P = run_on<ST>(sm.run[i], P);
+      }
+      if (lane == 0 && p.group == 1) put_state(p.states + row * p.groups + at.time, P);
+      if (lane == 0 && at.time == p.tiles - 1 && p.dh0) p.dh0[row] = P;
+    }
+    __syncthreads();
+    const float pw = sm.in[w];
+    float db = lane_grads<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, dh, b2, hin,
+                                          lane == 31 ? pw : run_on<ST>(after, pw), hv.lo, gv.hi, t < p.L);
+    if (p.dbias_part) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) db += __shfl_xor_sync(kAll, db, o);
+      if (lane == 0) sm.db[w] = db;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGsTileWarps; ++i) s += sm.db[i];
+        p.dbias_part[((int64_t)at.batch * p.tiles + (p.tiles - 1 - at.time)) * p.dim + at.rest] = s;
+      }
+    }
+    __syncwarp();
+    if (next_ticket >= total) break;
+    at = next;
   }
 }
 
 // ---- launches -----------------------------------------------------------------------------
+template <typename K>
+cudaError_t with_smem(K kern, int smem) {
+  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+}
+
 template <typename T, bool TIED, bool Z, bool ST>
 cudaError_t launch_t(bool bwd, int path, const GsParams &p, cudaStream_t s) {
   const int64_t rows = p.batch * p.dim;
+  cudaError_t e;
   if (path == SSM_PATH_LOOKBACK) {
-    const int64_t n = rows * p.tiles;
-    if (n > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (bwd) k_tiles_bwd<T, TIED, Z, ST><<<(unsigned)n, kTileThreads, 0, s>>>(p);
-    else k_tiles_fwd<T, TIED, Z, ST><<<(unsigned)n, kTileThreads, 0, s>>>(p);
+    const int smem = kGsTileWarps * 2 * (bwd ? kStage<Z, true> : kStage<Z, false>);
+    auto kern = bwd ? k_tiles_bwd<T, TIED, Z, ST> : k_tiles_fwd<T, TIED, Z, ST>;
+    if ((e = with_smem(kern, smem)) != cudaSuccess) return e;
+    const int64_t n = std::min<int64_t>(rows * p.tiles, (int64_t)p.sms * (bwd ? 2 : 3));
+    kern<<<(unsigned)n, kTileThreads, smem, s>>>(p);
     return cudaGetLastError();
   }
   int W = 32;  // lanes per row: the fewest that hold a short row
   while (W > 1 && (int64_t)(W / 2) * Geo<T>::S >= p.L) W /= 2;
   const int64_t warps = (rows + 32 / W - 1) / (32 / W), blocks = (warps * 32 + kRowThreads - 1) / kRowThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (bwd) k_rows_bwd<T, TIED, Z, ST><<<(unsigned)blocks, kRowThreads, 0, s>>>(p, W);
-  else k_rows_fwd<T, TIED, Z, ST><<<(unsigned)blocks, kRowThreads, 0, s>>>(p, W);
+  const int smem = kRowThreads / 32 * (bwd ? kRowBwdStages * kStage<Z, true> : kRowStages * kStage<Z, false>);
+  auto kern = W == 32 ? (bwd ? k_rows_bwd<T, TIED, Z, ST, true> : k_rows_fwd<T, TIED, Z, ST, true>)
+                      : (bwd ? k_rows_bwd<T, TIED, Z, ST, false> : k_rows_fwd<T, TIED, Z, ST, false>);
+  if ((e = with_smem(kern, smem)) != cudaSuccess) return e;
+  kern<<<(unsigned)blocks, kRowThreads, smem, s>>>(p, W);
   return cudaGetLastError();
 }
 

@@ -1,100 +1,111 @@
 // Gated recurrence, token-major activations [batch][L][dim]: the channels of one
 // token are contiguous, as a projection leaves them.
 //
-// Memory bound like the channel-major form.  A lane takes a pair of channels, so
-// every step is one f32x2 operation and a warp's access to a token is 128 bytes of
-// bf16 (256 of fp32); it walks kTokSteps / kTokWarps consecutive steps, held in
-// registers.  The warps of a block split a tile of kTokSteps steps of 64 channels and
-// join their runs through shared memory; tiles of the same channels hand their runs on
-// through the workspace (one tile: no waiting).
+// Memory bound like the channel-major form.  A lane takes a pair of channels, so every
+// step is one f32x2 operation, and walks kTokRun consecutive steps; the four warps of a block
+// split a tile of 64 channels by four such runs and join them through shared memory; tiles of
+// the same channels hand their runs on through the workspace.  Blocks stay and take tile after
+// tile: the next tile's ticket is drawn and its values are on their way into shared memory
+// (cp.async, each warp its own steps) while the current one is worked on.
 #include "ssm_gscan.cuh"
+
+#include <algorithm>
 
 namespace ssm {
 
 namespace {
 
-constexpr int kTokWarps = 8;
+constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTokThreads = 32 * kTokWarps;
-constexpr int kTokRun = kTokSteps / kTokWarps;  // steps per warp
-static_assert(kTokGroup <= 2 * kTokWarps, "a warp waits for two tiles at most");
-
-// a pair of channels of one token as loaded
-template <typename T> struct Raw;
-template <> struct Raw<uint16_t> {
-  uint32_t v;
-  __device__ __forceinline__ f2 get() const { return pack2(bf16_lo(v), bf16_hi(v)); }
-};
-template <> struct Raw<float> {
-  float2 v;
-  __device__ __forceinline__ f2 get() const { return pack2(v.x, v.y); }
-};
-
-// The lane's channels: neighbours (2l, 2l + 1) where pairs are aligned, else l and
-// l + 32, each access a warp-wide run either way.
-struct Pair {
-  int64_t d0, d1;
-  bool in0, in1, vec;
-};
-__device__ __forceinline__ Pair pair_of(const GsParams &p, int64_t cg, int lane) {
-  Pair c;
-  c.vec = p.vec != 0;
-  c.d0 = cg * kTokChannels + (c.vec ? 2 * lane : lane);
-  c.d1 = c.d0 + (c.vec ? 1 : 32);
-  c.in0 = c.d0 < p.dim;
-  c.in1 = c.d1 < p.dim;
-  return c;
-}
+constexpr int kTokFwdBlocks = 4, kTokBwdBlocks = 3;  // an SM: their shared memory and registers fit
+static_assert(kTokGroup <= 4 * kTokWarps, "a warp waits for four tiles at most");
 
 template <typename T>
-__device__ __forceinline__ Raw<T> load_pair(const void *base, int64_t tok, const GsParams &p, const Pair &c, bool in) {
-  Raw<T> r;
-  const T *q = static_cast<const T *>(base) + tok * p.dim;
+struct Tok {
+  static constexpr int RUN = gs_tok_steps(sizeof(T)) / kTokWarps;  // steps per warp
+  static constexpr int ROW = kTokChannels * (int)sizeof(T);        // bytes of a token's channels
+  static constexpr int SLOT = RUN * ROW;                           // a warp's piece of one tensor
+};
+static_assert(Tok<uint16_t>::SLOT == 2048 && Tok<float>::SLOT == 2048, "slots are laid out alike");
+
+template <bool Z, bool BWD>
+constexpr int kWarpStage = 2048 * (2 + (Z ? 1 : 0) + (BWD ? 1 : 0));
+constexpr int kTokF = 0, kTokU = 2048, kTokZ = 4096;
+template <bool Z>
+constexpr int kTokG = Z ? 6144 : 4096;
+
+// the lane's pair of channels at step i of a slot
+template <typename T>
+__device__ __forceinline__ f2 pair_at(const unsigned char *slot, int i, int lane) {
   if constexpr (sizeof(T) == 2) {
-    r.v = 0u;
-    if (c.vec) {
-      if (in && c.in0) r.v = __ldcs(reinterpret_cast<const uint32_t *>(q + c.d0));
-    } else {
-      if (in && c.in0) r.v = q[c.d0];
-      if (in && c.in1) r.v |= (uint32_t)q[c.d1] << 16;
-    }
+    const uint32_t v = *reinterpret_cast<const uint32_t *>(slot + i * Tok<T>::ROW + 4 * lane);
+    return pack2(bf16_lo(v), bf16_hi(v));
   } else {
-    r.v = make_float2(0.f, 0.f);
-    if (c.vec) {
-      if (in && c.in0) r.v = __ldcs(reinterpret_cast<const float2 *>(q + c.d0));
-    } else {
-      if (in && c.in0) r.v.x = q[c.d0];
-      if (in && c.in1) r.v.y = q[c.d1];
-    }
+    return *reinterpret_cast<const f2 *>(slot + i * Tok<T>::ROW + 8 * lane);
   }
-  return r;
 }
 
+// Copies the warp's steps (n of them, from src: the first one's first channel of the group)
+// into a slot, zeros for steps and channels that are not there.  ch: channels of the group
+// there are.  mode 2: 16-byte pieces, 1: 4-byte words, 0: elements (not asynchronous).
 template <typename T>
-__device__ __forceinline__ void store_pair(void *base, int64_t tok, const GsParams &p, const Pair &c, bool in, f2 v) {
-  T *q = static_cast<T *>(base) + tok * p.dim;
-  float a, b;
-  unpack2(v, a, b);
-  if (!in) return;
-  if (c.vec) {
-    if (c.in0) {
-      if constexpr (sizeof(T) == 2) __stcs(reinterpret_cast<uint32_t *>(q + c.d0), pack_bf16x2(a, b));
-      else __stcs(reinterpret_cast<float2 *>(q + c.d0), make_float2(a, b));
+__device__ __forceinline__ void fill_slot(unsigned char *slot, const T *src, int n, int ch, int64_t dim, int mode, int lane) {
+  constexpr int RUN = Tok<T>::RUN, ROW = Tok<T>::ROW;
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
+  if (mode == 2) {
+    constexpr int E = 16 / (int)sizeof(T), PER = ROW / 16, STEP = 32 / PER;  // pieces a token, tokens a round
+    const int t = lane / PER, c = lane % PER * E;
+    const T *q = src + t * dim + c;
+#pragma unroll
+    for (int j = 0; j < RUN / STEP; ++j) {
+      const bool in = c < ch && t + j * STEP < n;
+      copy16(s + 16 * (j * 32 + lane), in ? q + j * STEP * dim : src, in);
+    }
+  } else if (mode == 1) {
+    constexpr int E = 4 / (int)sizeof(T), PER = ROW / 128;  // rounds a token
+#pragma unroll
+    for (int j = 0; j < RUN * PER; ++j) {
+      const int t = j / PER, c = (j % PER * 32 + lane) * E;
+      const bool in = c < ch && t < n;
+      copy4(s + 4 * (j * 32 + lane), in ? src + t * dim + c : src, in);
     }
   } else {
-    if (c.in0) IO<T>::store1(q, c.d0, a);
-    if (c.in1) IO<T>::store1(q, c.d1, b);
+#pragma unroll
+    for (int j = 0; j < 2 * RUN; ++j) {
+      const int t = j / 2, c = j % 2 * 32 + lane;
+      *reinterpret_cast<T *>(slot + t * ROW + c * (int)sizeof(T)) = c < ch && t < n ? src[t * dim + c] : T(0);
+    }
   }
 }
 
 // fp32 values of the lane's channels from a [..][dim] row (0 where absent), and back
+struct Pair {
+  int64_t d;       // the first one's channel
+  bool in0, in1;
+};
 __device__ __forceinline__ f2 load_f32(const float *row, const Pair &c) {
-  return pack2(row && c.in0 ? row[c.d0] : 0.f, row && c.in1 ? row[c.d1] : 0.f);
+  return pack2(row && c.in0 ? row[c.d] : 0.f, row && c.in1 ? row[c.d + 1] : 0.f);
 }
 __device__ __forceinline__ void store_f32(float *row, const Pair &c, f2 v) {
   float a, b;
   unpack2(v, a, b);
-  if (c.in0) row[c.d0] = a;
-  if (c.in1) row[c.d1] = b;
+  if (c.in0) row[c.d] = a;
+  if (c.in1) row[c.d + 1] = b;
+}
+// a step's pair to q (the lane's first channel); pairs: one aligned access
+template <typename T>
+__device__ __forceinline__ void put_pair(T *q, const Pair &c, bool pairs, f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  if (pairs) {
+    if (c.in0) {
+      if constexpr (sizeof(T) == 2) __stcs(reinterpret_cast<uint32_t *>(q), pack_bf16x2(a, b));
+      else __stcs(reinterpret_cast<float2 *>(q), make_float2(a, b));
+    }
+  } else {
+    if (c.in0) IO<T>::store1(q, 0, a);
+    if (c.in1) IO<T>::store1(q, 1, b);
+  }
 }
 
 // runs of the lane's two channels
@@ -124,11 +135,10 @@ __device__ __forceinline__ Run2 join2(const Run2 &own, const Run2 &other) {
 }
 
 // bit i: a sequence starts at the warp's step i
-template <bool ST>
-__device__ __forceinline__ unsigned warp_starts(const GsParams &p, int64_t b, int64_t t0, int lane) {
+template <typename T, bool ST>
+__device__ __forceinline__ unsigned warp_starts(const GsParams &p, int64_t tok, int n, int lane) {
   if constexpr (!ST) return 0u;
-  const int64_t t = t0 + lane;
-  return __ballot_sync(0xffffffffu, lane < kTokRun && t < p.L && p.starts[b * p.L + t]);
+  return __ballot_sync(kAll, lane < n && p.starts[tok + lane]);
 }
 
 // a start cuts the run, whatever its gates hold (NaN times 0)
@@ -143,263 +153,353 @@ __device__ __forceinline__ void cut_at_start(Run2 &r, unsigned st) {
 }
 
 struct TokShared {
-  unsigned slot;
+  unsigned next;
+  Place place;
   f2 A[kTokWarps][32], N[kTokWarps][32], B[kTokWarps][32];  // the warps' runs
-  unsigned long long run[kTokGroup][64];                    // the runs of the group's earlier tiles
-  f2 in[32];                                                // the state entering the tile
-  f2 other[kTokWarps][32];
+  f2 other[kTokWarps][32];                                  // backward: B of the state's runs; sums
+  f2 in[32];                                                // the value entering the tile
   __device__ __forceinline__ Run2 of(int w, int lane) const { return {A[w][lane], N[w][lane], B[w][lane]}; }
 };
 
-// Look-back of the whole block (see the channel-major form): `c` is the tile's index in
-// the direction of the walk, sm holds the warps' runs in that direction (warp 0 first, or
-// last with FROM_BEHIND).  Returns the value entering the warp's own run; `out` receives
-// in warp 0 the value leaving the tile.
-template <bool ST, bool FROM_BEHIND>
-__device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t chain, int64_t c, f2 first, int w,
-                                      int lane, f2 &out) {
-  const int64_t groups = (p.tiles + kTokGroup - 1) / kTokGroup, g = c / kTokGroup;
-  const int in = (int)(c - g * kTokGroup);
-  unsigned long long *runs = p.runs + chain * p.tiles * kTokChannels;
-  unsigned *states = p.states + chain * groups * kTokChannels;
-  const bool last = c == p.tiles - 1, last_in_group = in == kTokGroup - 1;
-  Run2 tile;
-  if (w == 0) {
-    tile = sm.of(FROM_BEHIND ? kTokWarps - 1 : 0, lane);
-#pragma unroll
-    for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(FROM_BEHIND ? kTokWarps - 1 - j : j, lane), tile);
-    if (!last && !last_in_group) {
-      Run x, y;
-      split(tile, x, y);
-      put_run(runs + c * kTokChannels + lane, x);
-      put_run(runs + c * kTokChannels + 32 + lane, y);
-    }
-  }
+// a pair of states as one word of 64 bits
+__device__ __forceinline__ void put_pair_state(unsigned long long *q, f2 v) {
+  float x, y;
+  unpack2(v, x, y);
+  const unsigned long long w = ((unsigned long long)as_word(y) << 32) | as_word(x);
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(q), "l"(w) : "memory");
+}
+__device__ __forceinline__ f2 of_pair(unsigned long long w) { return pack2(of_word((unsigned)w), of_word((unsigned)(w >> 32))); }
+__device__ __forceinline__ unsigned long long wait64(const unsigned long long *q, unsigned long long w, unsigned *err) {
   unsigned long long started = 0;
   unsigned n = 0;
-#pragma unroll
-  for (int j = w; j < kTokGroup; j += kTokWarps) {
-    if (j < in) {
-      const unsigned long long *q = runs + (g * kTokGroup + j) * kTokChannels + lane;
-      unsigned long long x, y;
-      while ((x = look64(q)) == 0ull)
-        if (!spun(started, n, p.err)) break;
-      while ((y = look64(q + 32)) == 0ull)
-        if (!spun(started, n, p.err)) break;
-      sm.run[j][lane] = x;
-      sm.run[j][32 + lane] = y;
-    }
+  while (w == 0ull) {
+    w = look64(q);
+    if (w == 0ull && !spun(started, n, err)) break;
   }
+  return w;
+}
+
+// Where the state that the tile's group starts from is (null in the first group)
+__device__ __forceinline__ const unsigned long long *state_of(const GsParams &p, int64_t chain, unsigned c, int lane) {
+  const unsigned g = c / p.group;
+  if (g == 0) return nullptr;
+  return reinterpret_cast<const unsigned long long *>(p.states) + (chain * p.groups + g - 1) * 32 + lane;
+}
+
+// Look-back of the whole block (see the channel-major form): `c` is the tile's index in
+// the direction of the walk, sm holds the warps' runs in that direction (warp 0 first, or
+// last with FROM_BEHIND), `seen` what the lane saw of the group's state when it looked
+// ahead.  Returns the value entering the warp's own run; `out` receives, in the warp that
+// the walk reaches last, the value leaving the tile.  With one tile a group (many chains: the
+// tile before was taken long ago) every warp reads the state itself; else the first warps
+// of the walk gather the runs of the group's tiles (`earlier`), in the order of their index.
+template <bool ST, bool FROM_BEHIND>
+__device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, unsigned long long (*earlier)[64], int64_t chain,
+                                      unsigned c, f2 first, int w, int lane, const unsigned long long *q, unsigned long long seen, f2 &out) {
+  const unsigned g = c / p.group, in = c - g * p.group;
+  const bool last = c == p.tiles - 1, last_in_group = in == p.group - 1;
+  const int mine = FROM_BEHIND ? kTokWarps - 1 - w : w;  // the warp's place in the walk
+  auto nth = [](int j) { return FROM_BEHIND ? kTokWarps - 1 - j : j; };
   f2 h = first;
-  if (w == 0 && g > 0) {
-    const unsigned *q = states + (g - 1) * kTokChannels + lane;
-    unsigned x, y;
-    while ((x = look32(q)) == 0u)
-      if (!spun(started, n, p.err)) break;
-    while ((y = look32(q + 32)) == 0u)
-      if (!spun(started, n, p.err)) break;
-    h = pack2(of_word(x), of_word(y));
-  }
-  if (in > 0) __syncthreads();
-  if (w == 0) {
-    float h0, h1;
-    unpack2(h, h0, h1);
-    for (int j = 0; j < in; ++j) {
-      h0 = run_on<ST>(of_words(sm.run[j][lane]), h0);
-      h1 = run_on<ST>(of_words(sm.run[j][32 + lane]), h1);
+  if (p.group == 1) {
+    if (q) h = of_pair(wait64(q, seen, p.err));
+  } else {
+    unsigned long long *runs = p.runs + chain * p.tiles * kTokChannels;
+    if (mine == 0) {
+      if (!last && !last_in_group) {
+        Run2 tile = sm.of(nth(0), lane);
+#pragma unroll
+        for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(nth(j), lane), tile);
+        Run x, y;
+        split(tile, x, y);
+        put_run(runs + (int64_t)c * kTokChannels + 2 * lane, x);
+        put_run(runs + (int64_t)c * kTokChannels + 2 * lane + 1, y);
+      }
+      if (q) h = of_pair(wait64(q, seen, p.err));
     }
-    h = pack2(h0, h1);
-    sm.in[lane] = h;
-    out = run_on2<ST>(tile, h);
-    if (!last && last_in_group) {
-      float x, y;
-      unpack2(out, x, y);
-      put_state(states + g * kTokChannels + lane, x);
-      put_state(states + g * kTokChannels + 32 + lane, y);
+    if (in > 0) {
+      for (unsigned j = mine; j < in; j += kTokWarps) {
+        const unsigned long long *a = runs + ((int64_t)g * p.group + j) * kTokChannels + 2 * lane;
+        earlier[j][2 * lane] = wait64(a, look64(a), p.err);
+        earlier[j][2 * lane + 1] = wait64(a + 1, look64(a + 1), p.err);
+      }
+      __syncthreads();
     }
+    if (mine == 0) {
+      float h0, h1;
+      unpack2(h, h0, h1);
+      for (unsigned j = 0; j < in; ++j) {
+        h0 = run_on<ST>(of_words(earlier[j][2 * lane]), h0);
+        h1 = run_on<ST>(of_words(earlier[j][2 * lane + 1]), h1);
+      }
+      sm.in[lane] = pack2(h0, h1);
+    }
+    __syncthreads();
+    h = sm.in[lane];
   }
-  __syncthreads();
-  h = sm.in[lane];
 #pragma unroll
   for (int j = 0; j < kTokWarps - 1; ++j) {
-    const int i = FROM_BEHIND ? kTokWarps - 1 - j : j;
-    if (FROM_BEHIND ? i <= w : i >= w) break;
-    h = run_on2<ST>(sm.of(i, lane), h);
+    if (j < mine) h = run_on2<ST>(sm.of(nth(j), lane), h);
+  }
+  if (mine == kTokWarps - 1) {
+    out = run_on2<ST>(sm.of(w, lane), h);
+    if (!last && last_in_group)
+      put_pair_state(reinterpret_cast<unsigned long long *>(p.states) + (chain * p.groups + g) * 32 + lane, out);
   }
   return h;
 }
 
-template <typename T, bool TIED, bool Z, bool ST>
-__global__ void __launch_bounds__(kTokThreads) k_tok_fwd(GsParams p) {
-  __shared__ TokShared sm;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t cgs = gs_tok_groups(p.dim), chains = p.batch * cgs;
-  const int64_t ticket = p.tiles > 1 ? take_ticket(p.ticket, &sm.slot) : blockIdx.x;
-  const int64_t c = ticket / chains, chain = ticket - c * chains, b = chain / cgs, cg = chain - b * cgs;
-  const Pair ch = pair_of(p, cg, lane);
-  const int64_t t0 = c * kTokSteps + w * kTokRun;
-  Raw<T> u[kTokRun], f[kTokRun], z[Z ? kTokRun : 1];
-#pragma unroll
-  for (int i = 0; i < kTokRun; ++i) {
-    const int64_t tok = b * p.L + t0 + i;
-    const bool in = t0 + i < p.L;
-    f[i] = load_pair<T>(p.f, tok, p, ch, in);
-    u[i] = load_pair<T>(p.u, tok, p, ch, in);
-    if constexpr (Z) z[i] = load_pair<T>(p.z, tok, p, ch, in);
+// A tile's place in the tensors, for one warp
+template <typename T, bool FROM_BEHIND>
+struct Where {
+  int64_t time, t0, tok;  // tile along time, the warp's first step, and its token
+  int n;                  // steps of the warp there are
+  int ch;                 // channels of the group there are
+  int64_t first;          // element index of the warp's first step and the group's first channel
+  __device__ __forceinline__ Where(const GsParams &p, const Place &a, int w) {
+    time = FROM_BEHIND ? p.tiles - 1 - a.time : a.time;
+    t0 = time * gs_tok_steps(sizeof(T)) + w * Tok<T>::RUN;
+    tok = (int64_t)a.batch * p.L + t0;
+    const int64_t left = p.L - t0, c = p.dim - (int64_t)a.rest * kTokChannels;
+    n = left < 0 ? 0 : left < Tok<T>::RUN ? (int)left : Tok<T>::RUN;
+    ch = c < kTokChannels ? (int)c : kTokChannels;
+    first = tok * p.dim + (int64_t)a.rest * kTokChannels;
   }
-  const unsigned st = warp_starts<ST>(p, b, t0, lane);
-  const f2 b2 = mul2(load_f32(p.bias, ch), splat2(kLog2e));
-  const f2 first = load_f32(p.h0 ? p.h0 + b * p.dim : nullptr, ch);
-  f2 ng[kTokRun];
+};
+
+template <typename T, bool Z, bool BWD>
+__device__ __forceinline__ void fill_stage(unsigned char *st, const GsParams &p, const Where<T, BWD> &a, int lane) {
+  // a warp with no steps copies nothing from, but its pointers have to be inside
+  const int64_t at = a.n > 0 ? a.first : 0;
+  fill_slot<T>(st + kTokF, static_cast<const T *>(p.f) + at, a.n, a.ch, p.dim, p.vec, lane);
+  fill_slot<T>(st + kTokU, static_cast<const T *>(p.u) + at, a.n, a.ch, p.dim, p.vec, lane);
+  if constexpr (Z) fill_slot<T>(st + kTokZ, static_cast<const T *>(p.z) + at, a.n, a.ch, p.dim, p.vec, lane);
+  if constexpr (BWD) fill_slot<T>(st + kTokG<Z>, static_cast<const T *>(p.dout) + at, a.n, a.ch, p.dim, p.vec, lane);
+}
+
+// -g of the warp's steps and their run on the state; steps past the end hold it (g = 0)
+template <typename T, bool TIED, bool ST>
+__device__ __forceinline__ Run2 warp_run(f2 (&ng)[Tok<T>::RUN], const unsigned char *stage, int n, f2 b2, unsigned st, int lane) {
   Run2 r = {splat2(1.f), splat2(0.f), splat2(0.f)};
 #pragma unroll
-  for (int i = 0; i < kTokRun; ++i) {
-    ng[i] = t0 + i < p.L ? neg_gate2(f[i].get(), b2) : splat2(0.f);  // a step past the end holds the state
+  for (int i = 0; i < Tok<T>::RUN; ++i) {
+    ng[i] = neg_gate2(pair_at<T>(stage + kTokF, i, lane), b2);
+    if (i >= n) ng[i] = splat2(0.f);
     if constexpr (ST) {
       if ((st >> i) & 1u) r.B = splat2(0.f);
     }
-    r.B = state_step<TIED>(r.B, ng[i], u[i].get());
+    r.B = state_step<TIED>(r.B, ng[i], pair_at<T>(stage + kTokU, i, lane));
     r.N = fma2(ng[i], r.A, r.N);
     r.A = fma2(ng[i], r.A, r.A);
   }
   cut_at_start<ST>(r, st);
-  sm.A[w][lane] = r.A;
-  sm.N[w][lane] = r.N;
-  sm.B[w][lane] = r.B;
-  __syncthreads();
-  f2 out;
-  f2 h = tile_in<ST, false>(p, sm, chain, c, first, w, lane, out);
-  if (w == 0) {
-    if (p.ckpt) store_f32(p.ckpt + (b * p.tiles + c) * p.dim, ch, h);
-    if (p.last && c == p.tiles - 1) store_f32(p.last + b * p.dim, ch, out);
+  return r;
+}
+
+template <typename T, bool TIED, bool Z, bool ST>
+__global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams p) {
+  constexpr int RUN = Tok<T>::RUN, STAGE = kWarpStage<Z, false>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ TokShared sm;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  unsigned char *ring = smem + w * 2 * STAGE;
+  auto earlier = reinterpret_cast<unsigned long long (*)[64]>(smem + kTokWarps * 2 * STAGE);  // with groups of tiles
+  const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
+  if (threadIdx.x == 0) {
+    sm.next = p.ticket ? atomicAdd(p.ticket, 1u) : blockIdx.x;
+    sm.place = place_of(sm.next, chains, cgs);
   }
-  if (!p.y) return;
+  __syncthreads();
+  if (sm.next >= total) return;
+  Place at = sm.place;
+  __syncthreads();  // before the next ticket takes its place
+  fill_stage<T, Z, false>(ring, p, Where<T, false>(p, at, w), lane);
+  copies_commit();
+  for (int stg = 0;; stg ^= 1) {
+    const Where<T, false> a(p, at, w);
+    const unsigned char *stage = ring + stg * STAGE;
+    unsigned drawn = total;
+    if (threadIdx.x == 0 && p.ticket) drawn = atomicAdd(p.ticket, 1u);
+    const unsigned long long *q = state_of(p, at.chain, at.time, lane);
+    const unsigned long long seen = q ? look64(q) : 0ull;
+    const Pair ch = {(int64_t)at.rest * kTokChannels + 2 * lane, 2 * lane < a.ch, 2 * lane + 1 < a.ch};
+    const f2 b2 = mul2(load_f32(p.bias, ch), splat2(kLog2e));
+    const f2 first = load_f32(p.h0 ? p.h0 + at.batch * p.dim : nullptr, ch);
+    const unsigned st = warp_starts<T, ST>(p, a.tok, a.n, lane);
+    copies_wait<0>();
+    __syncwarp();
+    f2 ng[RUN];
+    const Run2 r = warp_run<T, TIED, ST>(ng, stage, a.n, b2, st, lane);
+    sm.A[w][lane] = r.A;
+    sm.N[w][lane] = r.N;
+    sm.B[w][lane] = r.B;
+    if (threadIdx.x == 0) {
+      sm.next = drawn;
+      sm.place = place_of(drawn, chains, cgs);
+    }
+    __syncthreads();
+    const unsigned next_ticket = sm.next;
+    const Place next = sm.place;
+    if (next_ticket < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next, w), lane);
+    copies_commit();
+    f2 out;
+    f2 h = tile_in<ST, false>(p, sm, earlier, at.chain, at.time, first, w, lane, q, seen, out);
+    if (p.ckpt && w == 0) store_f32(p.ckpt + ((int64_t)at.batch * p.tiles + at.time) * p.dim, ch, h);
+    if (p.last && w == kTokWarps - 1 && at.time == p.tiles - 1) store_f32(p.last + at.batch * p.dim, ch, out);
+    if (p.y) {
+      T *y = static_cast<T *>(p.y) + a.first + 2 * lane;
 #pragma unroll
-  for (int i = 0; i < kTokRun; ++i) {
-    if constexpr (ST) {
-      if ((st >> i) & 1u) h = splat2(0.f);
+      for (int i = 0; i < RUN; ++i) {
+        if constexpr (ST) {
+          if ((st >> i) & 1u) h = splat2(0.f);
+        }
+        h = state_step<TIED>(h, ng[i], pair_at<T>(stage + kTokU, i, lane));
+        f2 o = h;
+        if constexpr (Z) {
+          const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
+          o = mul2(h, mul2(zv, sigmoid2(zv)));
+        }
+        if (i < a.n) put_pair<T>(y + i * p.dim, ch, p.v32, o);
+      }
     }
-    h = state_step<TIED>(h, ng[i], u[i].get());
-    f2 o = h;
-    if constexpr (Z) {
-      const f2 zv = z[i].get();
-      o = mul2(h, mul2(zv, sigmoid2(zv)));
-    }
-    store_pair<T>(p.y, b * p.L + t0 + i, p, ch, t0 + i < p.L, o);
+    if (next_ticket >= total) break;
+    at = next;
+    __syncthreads();  // every warp is done with the tile's runs
   }
 }
 
 template <typename T, bool TIED, bool Z, bool ST>
-__global__ void __launch_bounds__(kTokThreads, 2) k_tok_bwd(GsParams p) {
+__global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams p) {
+  constexpr int RUN = Tok<T>::RUN, STAGE = kWarpStage<Z, true>;
+  extern __shared__ __align__(16) unsigned char smem[];
   __shared__ TokShared sm;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t cgs = gs_tok_groups(p.dim), chains = p.batch * cgs;
-  const int64_t ticket = p.tiles > 1 ? take_ticket(p.ticket, &sm.slot) : blockIdx.x;
-  const int64_t cb = ticket / chains, chain = ticket - cb * chains, b = chain / cgs, cg = chain - b * cgs;
-  const int64_t c = p.tiles - 1 - cb;  // from behind
-  const Pair ch = pair_of(p, cg, lane);
-  const int64_t t0 = c * kTokSteps + w * kTokRun;
-  Raw<T> u[kTokRun], f[kTokRun], g[kTokRun], z[Z ? kTokRun : 1];
-#pragma unroll
-  for (int i = 0; i < kTokRun; ++i) {
-    const int64_t tok = b * p.L + t0 + i;
-    const bool in = t0 + i < p.L;
-    f[i] = load_pair<T>(p.f, tok, p, ch, in);
-    u[i] = load_pair<T>(p.u, tok, p, ch, in);
-    g[i] = load_pair<T>(p.dout, tok, p, ch, in);
-    if constexpr (Z) z[i] = load_pair<T>(p.z, tok, p, ch, in);
+  unsigned char *ring = smem + w * 2 * STAGE;
+  auto earlier = reinterpret_cast<unsigned long long (*)[64]>(smem + kTokWarps * 2 * STAGE);  // with groups of tiles
+  const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
+  if (threadIdx.x == 0) {
+    sm.next = p.ticket ? atomicAdd(p.ticket, 1u) : blockIdx.x;
+    sm.place = place_of(sm.next, chains, cgs);
   }
-  const unsigned st = warp_starts<ST>(p, b, t0, lane);
-  const f2 b2 = mul2(load_f32(p.bias, ch), splat2(kLog2e));
-  const float *hrow = c > 0 ? p.ckpt + (b * p.tiles + c) * p.dim : p.h0 ? p.h0 + b * p.dim : nullptr;
-  f2 h = load_f32(hrow, ch);
-  const f2 first = load_f32(p.dlast ? p.dlast + b * p.dim : nullptr, ch);
-  // the states: runs of the warps before this one, then its own steps.  A and N are
-  // shared with the gradient's runs below.
-  f2 ng[kTokRun];
-  Run2 r = {splat2(1.f), splat2(0.f), splat2(0.f)};
-#pragma unroll
-  for (int i = 0; i < kTokRun; ++i) {
-    ng[i] = t0 + i < p.L ? neg_gate2(f[i].get(), b2) : splat2(0.f);
-    if constexpr (ST) {
-      if ((st >> i) & 1u) r.B = splat2(0.f);
-    }
-    r.B = state_step<TIED>(r.B, ng[i], u[i].get());
-    r.N = fma2(ng[i], r.A, r.N);
-    r.A = fma2(ng[i], r.A, r.A);
-  }
-  cut_at_start<ST>(r, st);
-  // the gradient's run from behind
-  f2 R = splat2(0.f), dh[kTokRun];
-#pragma unroll
-  for (int i = kTokRun - 1; i >= 0; --i) {
-    dh[i] = g[i].get();
-    if constexpr (Z) {
-      const f2 zv = z[i].get();
-      dh[i] = mul2(dh[i], mul2(zv, sigmoid2(zv)));
-    }
-    const f2 s = add2(dh[i], R);
-    R = fma2(ng[i], s, s);
-    if constexpr (ST) {
-      if ((st >> i) & 1u) R = splat2(0.f);
-    }
-  }
-  sm.A[w][lane] = r.A;
-  sm.N[w][lane] = r.N;
-  sm.B[w][lane] = R;
-  sm.other[w][lane] = r.B;
   __syncthreads();
-  for (int i = 0; i < w; ++i) h = run_on2<ST>({sm.A[i][lane], sm.N[i][lane], sm.other[i][lane]}, h);
-  f2 out;
-  f2 P = tile_in<ST, true>(p, sm, chain, cb, first, w, lane, out);
-  if (w == 0 && p.dh0 && c == 0) store_f32(p.dh0 + b * p.dim, ch, out);
-  f2 wt[kTokRun];
+  if (sm.next >= total) return;
+  Place at = sm.place;
+  __syncthreads();  // before the next ticket takes its place
+  fill_stage<T, Z, true>(ring, p, Where<T, true>(p, at, w), lane);
+  copies_commit();
+  for (int stg = 0;; stg ^= 1) {
+    const Where<T, true> a(p, at, w);
+    const unsigned char *stage = ring + stg * STAGE;
+    unsigned drawn = total;
+    if (threadIdx.x == 0 && p.ticket) drawn = atomicAdd(p.ticket, 1u);
+    const unsigned long long *q = state_of(p, at.chain, at.time, lane);
+    const unsigned long long seen = q ? look64(q) : 0ull;
+    const Pair ch = {(int64_t)at.rest * kTokChannels + 2 * lane, 2 * lane < a.ch, 2 * lane + 1 < a.ch};
+    const f2 b2 = mul2(load_f32(p.bias, ch), splat2(kLog2e));
+    const float *hrow = a.time > 0 ? p.ckpt + ((int64_t)at.batch * p.tiles + a.time) * p.dim
+                                   : p.h0 ? p.h0 + at.batch * p.dim : nullptr;
+    f2 h = load_f32(hrow, ch);
+    const f2 first = load_f32(p.dlast ? p.dlast + at.batch * p.dim : nullptr, ch);
+    const unsigned st = warp_starts<T, ST>(p, a.tok, a.n, lane);
+    copies_wait<0>();
+    __syncwarp();
+    // the state's run, and the gradient's from behind, which shares A and N with it
+    f2 ng[RUN], dh[RUN];
+    const Run2 r = warp_run<T, TIED, ST>(ng, stage, a.n, b2, st, lane);
+    f2 R = splat2(0.f);
 #pragma unroll
-  for (int i = 0; i < kTokRun; ++i) {
-    if constexpr (ST) {
-      if ((st >> i) & 1u) h = splat2(0.f);
+    for (int i = RUN - 1; i >= 0; --i) {
+      dh[i] = pair_at<T>(stage + kTokG<Z>, i, lane);
+      if constexpr (Z) {
+        const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
+        dh[i] = mul2(dh[i], mul2(zv, sigmoid2(zv)));
+      }
+      const f2 s = add2(dh[i], R);
+      R = fma2(ng[i], s, s);
+      if constexpr (ST) {
+        if ((st >> i) & 1u) R = splat2(0.f);
+      }
     }
-    const f2 uv = u[i].get(), ag = gate_slope2(f[i].get(), b2, ng[i]);
-    wt[i] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
-    h = state_step<TIED>(h, ng[i], uv);
-    if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
-      const f2 zv = z[i].get(), s = sigmoid2(zv);
-      const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
-      store_pair<T>(p.dz, b * p.L + t0 + i, p, ch, t0 + i < p.L, mul2(mul2(g[i].get(), h), mul2(s, k)));
+    sm.A[w][lane] = r.A;
+    sm.N[w][lane] = r.N;
+    sm.B[w][lane] = R;
+    sm.other[w][lane] = r.B;
+    if (threadIdx.x == 0) {
+      sm.next = drawn;
+      sm.place = place_of(drawn, chains, cgs);
     }
-  }
-  f2 sum = splat2(0.f);
-#pragma unroll
-  for (int i = kTokRun - 1; i >= 0; --i) {
-    const bool in = t0 + i < p.L;
-    const f2 G = add2(dh[i], P), df = mul2(G, wt[i]);
-    store_pair<T>(p.du, b * p.L + t0 + i, p, ch, in, TIED ? mul2(mul2(G, ng[i]), splat2(-1.f)) : G);
-    store_pair<T>(p.df, b * p.L + t0 + i, p, ch, in, df);
-    if (in) sum = add2(sum, df);
-    P = fma2(ng[i], G, G);
-    if constexpr (ST) {
-      if ((st >> i) & 1u) P = splat2(0.f);
-    }
-  }
-  if (p.dbias_part) {
-    __syncthreads();  // every warp has read the states' runs
-    sm.other[w][lane] = sum;
     __syncthreads();
-    if (w == 0) {
-      f2 t = splat2(0.f);
+    const unsigned next_ticket = sm.next;
+    const Place next = sm.place;
+    if (next_ticket < total) fill_stage<T, Z, true>(ring + (stg ^ 1) * STAGE, p, Where<T, true>(p, next, w), lane);
+    copies_commit();
 #pragma unroll
-      for (int i = 0; i < kTokWarps; ++i) t = add2(t, sm.other[i][lane]);
-      store_f32(p.dbias_part + (b * p.tiles + c) * p.dim, ch, t);
+    for (int i = 0; i < kTokWarps - 1; ++i) {
+      if (i < w) h = run_on2<ST>({sm.A[i][lane], sm.N[i][lane], sm.other[i][lane]}, h);
     }
+    f2 out;
+    f2 P = tile_in<ST, true>(p, sm, earlier, at.chain, at.time, first, w, lane, q, seen, out);
+    if (p.dh0 && w == 0 && a.time == 0) store_f32(p.dh0 + at.batch * p.dim, ch, out);
+    const int64_t e0 = a.first + 2 * lane;
+    f2 wt[RUN];
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      if constexpr (ST) {
+        if ((st >> i) & 1u) h = splat2(0.f);
+      }
+      const f2 uv = pair_at<T>(stage + kTokU, i, lane);
+      const f2 ag = gate_slope2(pair_at<T>(stage + kTokF, i, lane), b2, ng[i]);
+      wt[i] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
+      h = state_step<TIED>(h, ng[i], uv);
+      if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
+        const f2 zv = pair_at<T>(stage + kTokZ, i, lane), s = sigmoid2(zv);
+        const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
+        const f2 o = mul2(mul2(pair_at<T>(stage + kTokG<Z>, i, lane), h), mul2(s, k));
+        if (i < a.n) put_pair<T>(static_cast<T *>(p.dz) + e0 + i * p.dim, ch, p.v32, o);
+      }
+    }
+    f2 sum = splat2(0.f);
+#pragma unroll
+    for (int i = RUN - 1; i >= 0; --i) {
+      const f2 G = add2(dh[i], P), df = mul2(G, wt[i]);
+      if (i < a.n) {
+        put_pair<T>(static_cast<T *>(p.du) + e0 + i * p.dim, ch, p.v32, TIED ? mul2(mul2(G, ng[i]), splat2(-1.f)) : G);
+        put_pair<T>(static_cast<T *>(p.df) + e0 + i * p.dim, ch, p.v32, df);
+        sum = add2(sum, df);
+      }
+      P = fma2(ng[i], G, G);
+      if constexpr (ST) {
+        if ((st >> i) & 1u) P = splat2(0.f);
+      }
+    }
+    __syncthreads();  // every warp is done with the tile's runs
+    if (p.dbias_part) {
+      sm.other[w][lane] = sum;
+      __syncthreads();
+      if (w == 0) {
+        f2 t = splat2(0.f);
+#pragma unroll
+        for (int i = 0; i < kTokWarps; ++i) t = add2(t, sm.other[i][lane]);
+        store_f32(p.dbias_part + ((int64_t)at.batch * p.tiles + a.time) * p.dim, ch, t);
+      }
+    }
+    if (next_ticket >= total) break;
+    at = next;
+    if (p.dbias_part) __syncthreads();
   }
 }
 
 template <typename T, bool TIED, bool Z, bool ST>
 cudaError_t launch_t(bool bwd, const GsParams &p, cudaStream_t s) {
   const int64_t n = p.batch * gs_tok_groups(p.dim) * p.tiles;
-  if (n > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (bwd) k_tok_bwd<T, TIED, Z, ST><<<(unsigned)n, kTokThreads, 0, s>>>(p);
-  else k_tok_fwd<T, TIED, Z, ST><<<(unsigned)n, kTokThreads, 0, s>>>(p);
+  const int smem = kTokWarps * 2 * (bwd ? kWarpStage<Z, true> : kWarpStage<Z, false>) +
+                   (p.group > 1 ? kTokGroup * 64 * (int)sizeof(unsigned long long) : 0);
+  auto kern = bwd ? k_tok_bwd<T, TIED, Z, ST> : k_tok_fwd<T, TIED, Z, ST>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // without tickets (one tile a chain) every block has one tile
+  const int64_t blocks = p.ticket ? std::min<int64_t>(n, (int64_t)p.sms * (bwd ? kTokBwdBlocks : kTokFwdBlocks)) : n;
+  kern<<<(unsigned)blocks, kTokThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 

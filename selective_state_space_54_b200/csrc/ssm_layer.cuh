@@ -22,13 +22,16 @@ __host__ __device__ __forceinline__ int64_t gs_row_chunks(int64_t L, int esize) 
   return (L + gs_row_steps(esize) - 1) / gs_row_steps(esize);
 }
 constexpr int kGsTileWarps = 8;    // warps, and warp runs of steps, per look-back tile
-constexpr int kGsRowGroup = 32;    // tiles between two published states of a row
-// Token-major: a tile is kTokSteps steps of kTokChannels channels.  Saved
-// [batch][tile][dim] fp32, the state entering every tile.
+constexpr int kGsRowGroup = 31;    // tiles between two published states of a row, at most
+// Token-major: a tile is 64 channels by gs_tok_steps steps (8 KB of each tensor), a warp's
+// run a quarter of it.  Saved [batch][tile][dim] fp32, the state entering every tile.
 constexpr int kTokChannels = 64;
-constexpr int kTokSteps = 64;
-constexpr int kTokGroup = 16;      // tiles between two published states of a channel
-__host__ __device__ __forceinline__ int64_t gs_tok_tiles(int64_t L) { return (L + kTokSteps - 1) / kTokSteps; }
+constexpr int kTokWarps = 4;
+constexpr int kTokGroup = 16;      // tiles between two published states of a channel, at most
+__host__ __device__ constexpr int gs_tok_steps(int esize) { return 128 / esize; }
+__host__ __device__ __forceinline__ int64_t gs_tok_tiles(int64_t L, int esize) {
+  return (L + gs_tok_steps(esize) - 1) / gs_tok_steps(esize);
+}
 __host__ __device__ __forceinline__ int64_t gs_tok_groups(int64_t dim) { return (dim + kTokChannels - 1) / kTokChannels; }
 
 struct GsParams {
@@ -41,14 +44,16 @@ struct GsParams {
   float *ckpt;                       // saved states, nullable (forward writes, backward reads)
   int64_t batch, dim, L;
   int tok, untied;
-  int vec;                           // rows: 2 = 32-byte, 1 = 16-byte aligned, 0 = neither;
-                                     // token-major: channel pairs aligned
+  int vec;                           // accesses rows allow: 2 = 16 bytes, 1 = 4, 0 = one element
+  int v32;                           // channel-major: 32-byte stores
   int start_vec;                     // starts rows 16-byte aligned
   // look-back schedule (zeroed): error word, ticket counter, tile runs, group states
   unsigned *err, *ticket;
   unsigned long long *runs;
   unsigned *states;
   int64_t tiles;                     // time tiles per row or channel group
+  unsigned group, groups;            // tiles between two published states, and how many such groups
+  int sms;
   // backward
   const void *dout;
   const float *dlast;                // [batch][dim], nullable

@@ -43,7 +43,8 @@ ssm_status check_gscan(const ssm_shape *s) {
 // before each launch), then the partial sums of df_bias.
 struct GsPlan {
   int path = SSM_PATH_PER_GROUP;
-  int64_t tiles = 1, part_rows = 0;
+  int64_t tiles = 1, group = 1, groups = 1, part_rows = 0;
+  int sms = 0;
   size_t ckpt_bytes = 0;
   size_t off_ctl = 0, off_runs = 0, off_states = 0, end_ctl = 0;  // look-back
   size_t off_part = 0, total = 0;
@@ -53,6 +54,7 @@ struct GsPlan {
 // (each holds two passes of its row in flight); with fewer, rows longer than one tile
 // are split into tiles.
 constexpr int64_t kRowsPerSm = 8;
+constexpr int64_t kTilesPerSm = 4;  // tiles an SM works on at once
 
 ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   GsPlan l;
@@ -61,29 +63,32 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   const int64_t rows = s->batch * s->dim, L = s->seqlen;
   const int64_t row_tile = (int64_t)kGsTileWarps * gs_row_steps(es);
   l.path = tok ? SSM_PATH_LOOKBACK : s->path;
-  if (l.path == SSM_PATH_AUTO) {
-    l.path = SSM_PATH_PER_GROUP;
-    if (L > row_tile) {
-      const int sms = device_sms();
-      if (sms <= 0) return SSM_ERR_CUDA;
-      if (rows < kRowsPerSm * sms) l.path = SSM_PATH_LOOKBACK;
-    }
+  if (l.path == SSM_PATH_AUTO && L <= row_tile) l.path = SSM_PATH_PER_GROUP;
+  if (l.path != SSM_PATH_PER_GROUP) {
+    l.sms = device_sms();
+    if (l.sms <= 0) return SSM_ERR_CUDA;
+    if (l.path == SSM_PATH_AUTO) l.path = rows < kRowsPerSm * l.sms ? SSM_PATH_LOOKBACK : SSM_PATH_PER_GROUP;
   }
   const int64_t chains = tok ? s->batch * gs_tok_groups(s->dim) : rows;  // sequences of tiles
-  const int64_t width = tok ? kTokChannels : 1, group = tok ? kTokGroup : kGsRowGroup;
-  if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L) : (L + row_tile - 1) / row_tile;
+  const int64_t width = tok ? kTokChannels : 1;
+  if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L, es) : (L + row_tile - 1) / row_tile;
   if ((double)chains * (double)l.tiles > 2.0e9) return SSM_ERR_UNSUPPORTED;  // a grid dimension
+  // Tiles between two published states: one where there are more chains than tiles at work
+  // (the tile before was taken a whole round ago: its state is there), else many, so that a
+  // chain's state takes few steps from tile to tile.
+  if (chains < kTilesPerSm * (int64_t)l.sms) l.group = tok ? kTokGroup : kGsRowGroup;
+  l.groups = (l.tiles + l.group - 1) / l.group;
   l.part_rows = s->batch * (l.path == SSM_PATH_LOOKBACK ? l.tiles : 1);
   const bool save = bwd || (s->flags & SSM_FLAG_SAVE_STATES);
   if (save)
-    l.ckpt_bytes = round_up(sizeof(float) * (size_t)rows * (size_t)(tok ? gs_tok_tiles(L) : gs_row_chunks(L, es)), 256);
+    l.ckpt_bytes = round_up(sizeof(float) * (size_t)rows * (size_t)(tok ? gs_tok_tiles(L, es) : gs_row_chunks(L, es)), 256);
   size_t at = kHeaderBytes + l.ckpt_bytes;
   const bool handoff = l.path == SSM_PATH_LOOKBACK && !(tok && l.tiles == 1);
   if (handoff) {
     l.off_ctl = at;
     l.off_runs = l.off_ctl + 256;
-    l.off_states = l.off_runs + sizeof(unsigned long long) * (size_t)chains * (size_t)l.tiles * width;
-    at = l.off_states + sizeof(unsigned) * (size_t)chains * (size_t)((l.tiles + group - 1) / group) * width;
+    l.off_states = l.off_runs + (l.group > 1 ? sizeof(unsigned long long) * (size_t)chains * (size_t)l.tiles * width : 0);
+    at = l.off_states + sizeof(unsigned) * (size_t)chains * (size_t)l.groups * width;
     l.end_ctl = at = round_up(at, 256);
   }
   if (bwd) {
@@ -98,6 +103,9 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
 // The control words of a launch zeroed, and their places set.
 cudaError_t gs_control(GsParams &p, const GsPlan &l, char *ws, cudaStream_t s) {
   p.tiles = l.tiles;
+  p.group = (unsigned)l.group;
+  p.groups = (unsigned)l.groups;
+  p.sms = l.sms;
   if (!ws) return cudaSuccess;
   p.err = reinterpret_cast<unsigned *>(ws);
   if (!l.end_ctl) return cudaMemsetAsync(ws, 0, sizeof(unsigned), s);
@@ -109,20 +117,18 @@ cudaError_t gs_control(GsParams &p, const GsPlan &l, char *ws, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaMemsetAsync(ws + l.off_ctl, 0, l.end_ctl - l.off_ctl, s);
 }
 
-// Widest access every given pointer and row allows: 32 or 16 bytes (channel-major rows),
-// or pairs of channels (token-major).
+// Widest access every given pointer and row allows: 16 bytes, 4, or one element; and whether
+// channel-major rows take 32-byte stores, token-major ones a pair of channels at once.
 void gs_access(GsParams &p, size_t es, std::initializer_list<const void *> ptrs) {
+  const size_t row = (size_t)(p.tok ? p.dim : p.L) * es;
   auto all = [&](size_t a) {
+    if (row % a) return false;
     for (const void *q : ptrs)
       if (!aligned(q, a)) return false;
     return true;
   };
-  if (p.tok) {
-    p.vec = p.dim % 2 == 0 && all(2 * es);
-  } else {
-    const size_t row = (size_t)p.L * es;
-    p.vec = row % 32 == 0 && all(32) ? 2 : row % 16 == 0 && all(16) ? 1 : 0;
-  }
+  p.vec = all(16) ? 2 : all(4) ? 1 : 0;
+  p.v32 = p.tok ? all(2 * es) : all(32);
   p.start_vec = p.starts && p.L % 4 == 0 && aligned(p.starts, 4);
 }
 
