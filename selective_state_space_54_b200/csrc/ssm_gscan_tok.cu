@@ -47,34 +47,41 @@ __device__ __forceinline__ f2 pair_at(const unsigned char *slot, int i, int lane
 
 // Copies the warp's steps (n of them, from src: the first one's first channel of the group)
 // into a slot, zeros for steps and channels that are not there.  ch: channels of the group
-// there are.  mode 2: 16-byte pieces, 1: 4-byte words, 0: elements (not asynchronous).
+// there are.  16-byte pieces (mode 2); out of line, to keep the tile's code short: 4-byte
+// words (mode 1) and elements (mode 0, not asynchronous).
 template <typename T>
-__device__ __forceinline__ void fill_slot(unsigned char *slot, const T *src, int n, int ch, int64_t dim, int mode, int lane) {
+__device__ __noinline__ void fill_slot_narrow(unsigned char *slot, const T *src, int n, int ch, int64_t dim, int mode, int lane) {
   constexpr int RUN = Tok<T>::RUN, ROW = Tok<T>::ROW;
-  const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
-  if (mode == 2) {
-    constexpr int E = 16 / (int)sizeof(T), PER = ROW / 16, STEP = 32 / PER;  // pieces a token, tokens a round
-    const int t = lane / PER, c = lane % PER * E;
-    const T *q = src + t * dim + c;
-#pragma unroll
-    for (int j = 0; j < RUN / STEP; ++j) {
-      const bool in = c < ch && t + j * STEP < n;
-      copy16(s + 16 * (j * 32 + lane), in ? q + j * STEP * dim : src, in);
-    }
-  } else if (mode == 1) {
+  if (mode == 1) {
     constexpr int E = 4 / (int)sizeof(T), PER = ROW / 128;  // rounds a token
-#pragma unroll
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
+#pragma unroll 4
     for (int j = 0; j < RUN * PER; ++j) {
       const int t = j / PER, c = (j % PER * 32 + lane) * E;
       const bool in = c < ch && t < n;
       copy4(s + 4 * (j * 32 + lane), in ? src + t * dim + c : src, in);
     }
   } else {
-#pragma unroll
+#pragma unroll 8
     for (int j = 0; j < 2 * RUN; ++j) {
       const int t = j / 2, c = j % 2 * 32 + lane;
       *reinterpret_cast<T *>(slot + t * ROW + c * (int)sizeof(T)) = c < ch && t < n ? src[t * dim + c] : T(0);
     }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void fill_slot(unsigned char *slot, const T *src, int n, int ch, int64_t dim, int mode, int lane) {
+  if (mode != 2) return fill_slot_narrow<T>(slot, src, n, ch, dim, mode, lane);
+  constexpr int E = 16 / (int)sizeof(T), PER = Tok<T>::ROW / 16, STEP = 32 / PER;  // pieces a token, tokens a round
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot) + 16 * lane;
+  const int t = lane / PER, c = lane % PER * E;
+  const T *q = src + t * dim + c;
+  const int left = c < ch ? n - t : 0;
+#pragma unroll
+  for (int j = 0; j < Tok<T>::RUN / STEP; ++j) {
+    const bool in = j * STEP < left;
+    copy16(s + 512 * j, in ? q : src, in);
+    q += STEP * dim;
   }
 }
 
@@ -92,19 +99,23 @@ __device__ __forceinline__ void store_f32(float *row, const Pair &c, f2 v) {
   if (c.in0) row[c.d] = a;
   if (c.in1) row[c.d + 1] = b;
 }
-// a step's pair to q (the lane's first channel); pairs: one aligned access
+// A step's pair to q, the lane's first channel.  all: the whole run is there and pairs are
+// aligned (one access; c.in0 as the predicate), else by elements, `in` telling whether the
+// step is there.
 template <typename T>
-__device__ __forceinline__ void put_pair(T *q, const Pair &c, bool pairs, f2 v) {
+__device__ __forceinline__ void put_pair(T *q, const Pair &c, bool all, bool in, f2 v) {
   float a, b;
   unpack2(v, a, b);
-  if (pairs) {
-    if (c.in0) {
-      if constexpr (sizeof(T) == 2) __stcs(reinterpret_cast<uint32_t *>(q), pack_bf16x2(a, b));
-      else __stcs(reinterpret_cast<float2 *>(q), make_float2(a, b));
+  if (all) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w = pack_bf16x2(a, b);
+      if (c.in0) __stcs(reinterpret_cast<uint32_t *>(q), w);
+    } else {
+      if (c.in0) __stcs(reinterpret_cast<float2 *>(q), make_float2(a, b));
     }
   } else {
-    if (c.in0) IO<T>::store1(q, 0, a);
-    if (c.in1) IO<T>::store1(q, 1, b);
+    if (in && c.in0) IO<T>::store1(q, 0, a);
+    if (in && c.in1) IO<T>::store1(q, 1, b);
   }
 }
 
@@ -282,9 +293,14 @@ template <typename T, bool TIED, bool ST>
 __device__ __forceinline__ Run2 warp_run(f2 (&ng)[Tok<T>::RUN], const unsigned char *stage, int n, f2 b2, unsigned st, int lane) {
   Run2 r = {splat2(1.f), splat2(0.f), splat2(0.f)};
 #pragma unroll
+  for (int i = 0; i < Tok<T>::RUN; ++i) ng[i] = neg_gate2(pair_at<T>(stage + kTokF, i, lane), b2);
+  if (n < Tok<T>::RUN) {
+#pragma unroll
+    for (int i = 0; i < Tok<T>::RUN; ++i)
+      if (i >= n) ng[i] = splat2(0.f);
+  }
+#pragma unroll
   for (int i = 0; i < Tok<T>::RUN; ++i) {
-    ng[i] = neg_gate2(pair_at<T>(stage + kTokF, i, lane), b2);
-    if (i >= n) ng[i] = splat2(0.f);
     if constexpr (ST) {
       if ((st >> i) & 1u) r.B = splat2(0.f);
     }
@@ -347,20 +363,25 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     if (p.ckpt && w == 0) store_f32(p.ckpt + ((int64_t)at.batch * p.tiles + at.time) * p.dim, ch, h);
     if (p.last && w == kTokWarps - 1 && at.time == p.tiles - 1) store_f32(p.last + at.batch * p.dim, ch, out);
     if (p.y) {
-      T *y = static_cast<T *>(p.y) + a.first + 2 * lane;
+      auto walk = [&](bool all) {
+        T *y = static_cast<T *>(p.y) + a.first + 2 * lane;
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        if constexpr (ST) {
-          if ((st >> i) & 1u) h = splat2(0.f);
+        for (int i = 0; i < RUN; ++i) {
+          if constexpr (ST) {
+            if ((st >> i) & 1u) h = splat2(0.f);
+          }
+          h = state_step<TIED>(h, ng[i], pair_at<T>(stage + kTokU, i, lane));
+          f2 o = h;
+          if constexpr (Z) {
+            const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
+            o = mul2(h, mul2(zv, sigmoid2(zv)));
+          }
+          put_pair<T>(y, ch, all, i < a.n, o);
+          y += p.dim;
         }
-        h = state_step<TIED>(h, ng[i], pair_at<T>(stage + kTokU, i, lane));
-        f2 o = h;
-        if constexpr (Z) {
-          const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
-          o = mul2(h, mul2(zv, sigmoid2(zv)));
-        }
-        if (i < a.n) put_pair<T>(y + i * p.dim, ch, p.v32, o);
-      }
+      };
+      if (p.v32 && a.n == RUN) walk(true);
+      else walk(false);
     }
     if (next_ticket >= total) break;
     at = next;
@@ -440,38 +461,45 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     f2 out;
     f2 P = tile_in<ST, true>(p, sm, earlier, at.chain, at.time, first, w, lane, q, seen, out);
     if (p.dh0 && w == 0 && a.time == 0) store_f32(p.dh0 + at.batch * p.dim, ch, out);
-    const int64_t e0 = a.first + 2 * lane;
-    f2 wt[RUN];
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      if constexpr (ST) {
-        if ((st >> i) & 1u) h = splat2(0.f);
-      }
-      const f2 uv = pair_at<T>(stage + kTokU, i, lane);
-      const f2 ag = gate_slope2(pair_at<T>(stage + kTokF, i, lane), b2, ng[i]);
-      wt[i] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
-      h = state_step<TIED>(h, ng[i], uv);
-      if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
-        const f2 zv = pair_at<T>(stage + kTokZ, i, lane), s = sigmoid2(zv);
-        const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
-        const f2 o = mul2(mul2(pair_at<T>(stage + kTokG<Z>, i, lane), h), mul2(s, k));
-        if (i < a.n) put_pair<T>(static_cast<T *>(p.dz) + e0 + i * p.dim, ch, p.v32, o);
-      }
-    }
     f2 sum = splat2(0.f);
+    auto walk = [&](bool all) {
+      f2 wt[RUN];
+      const int64_t e0 = a.first + 2 * lane;
+      T *dz = static_cast<T *>(p.dz) + e0;
 #pragma unroll
-    for (int i = RUN - 1; i >= 0; --i) {
-      const f2 G = add2(dh[i], P), df = mul2(G, wt[i]);
-      if (i < a.n) {
-        put_pair<T>(static_cast<T *>(p.du) + e0 + i * p.dim, ch, p.v32, TIED ? mul2(mul2(G, ng[i]), splat2(-1.f)) : G);
-        put_pair<T>(static_cast<T *>(p.df) + e0 + i * p.dim, ch, p.v32, df);
-        sum = add2(sum, df);
+      for (int i = 0; i < RUN; ++i) {
+        if constexpr (ST) {
+          if ((st >> i) & 1u) h = splat2(0.f);
+        }
+        const f2 uv = pair_at<T>(stage + kTokU, i, lane);
+        const f2 ag = gate_slope2(pair_at<T>(stage + kTokF, i, lane), b2, ng[i]);
+        wt[i] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
+        h = state_step<TIED>(h, ng[i], uv);
+        if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
+          const f2 zv = pair_at<T>(stage + kTokZ, i, lane), s = sigmoid2(zv);
+          const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
+          put_pair<T>(dz, ch, all, i < a.n, mul2(mul2(pair_at<T>(stage + kTokG<Z>, i, lane), h), mul2(s, k)));
+          dz += p.dim;
+        }
       }
-      P = fma2(ng[i], G, G);
-      if constexpr (ST) {
-        if ((st >> i) & 1u) P = splat2(0.f);
+      T *du = static_cast<T *>(p.du) + e0 + RUN * p.dim, *df = static_cast<T *>(p.df) + e0 + RUN * p.dim;
+#pragma unroll
+      for (int i = RUN - 1; i >= 0; --i) {
+        du -= p.dim;
+        df -= p.dim;
+        const bool in = i < a.n;
+        const f2 G = add2(dh[i], P), d = mul2(G, wt[i]);
+        put_pair<T>(du, ch, all, in, TIED ? mul2(G, mul2(ng[i], splat2(-1.f))) : G);
+        put_pair<T>(df, ch, all, in, d);
+        if (all || in) sum = add2(sum, d);
+        P = fma2(ng[i], G, G);
+        if constexpr (ST) {
+          if ((st >> i) & 1u) P = splat2(0.f);
+        }
       }
-    }
+    };
+    if (p.v32 && a.n == RUN) walk(true);
+    else walk(false);
     __syncthreads();  // every warp is done with the tile's runs
     if (p.dbias_part) {
       sm.other[w][lane] = sum;

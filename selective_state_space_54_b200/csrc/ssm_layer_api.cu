@@ -54,7 +54,7 @@ struct GsPlan {
 // (each holds two passes of its row in flight); with fewer, rows longer than one tile
 // are split into tiles.
 constexpr int64_t kRowsPerSm = 8;
-constexpr int64_t kTilesPerSm = 4;  // tiles an SM works on at once
+constexpr int64_t kTilesPerSm = 3;  // tiles an SM works on at once
 
 ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   GsPlan l;
