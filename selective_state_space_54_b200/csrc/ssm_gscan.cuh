@@ -185,8 +185,10 @@ __device__ __forceinline__ void copies_wait() {
 
 // Tile order.  Blocks take tiles by ticket, the tiles of one time index before those of
 // the next, so a tile that is waited for was taken earlier and is running or done (a block
-// takes its next tile before it has finished the current one, and finishes them in order).
-// One thread splits the ticket into the tile's time index, its chain (a row, or the channel
+// draws its next ticket while it works on a tile, and finishes its tiles in order: the lowest
+// unfinished ticket never waits).  Drawn two ahead, with the copies started an iteration
+// earlier, the tiles that others wait for lay longer in a block's hands: 1 x 1024 x 2^20 took
+// 2.01 instead of 1.80 ms.  One thread splits the ticket into the tile's time index, its chain (a row, or the channel
 // group of a batch element), and that into the batch element and what is left, in 32 bits
 // (the host checks that they fit): four 64-bit divisions in every thread cost more than the
 // gates.
@@ -200,6 +202,24 @@ __device__ __forceinline__ Place place_of(unsigned ticket, unsigned chains, unsi
   q.batch = q.chain / per_batch;
   q.rest = q.chain - q.batch * per_batch;
   return q;
+}
+// A ticket as thread 0 draws it and hands it out at a barrier of the block.
+struct Taken {
+  unsigned id;
+  Place place;
+};
+__device__ __forceinline__ void hand_out(Taken &t, unsigned id, unsigned chains, unsigned per_batch) {
+  t.id = id;
+  t.place = place_of(id, chains, per_batch);
+}
+// the first one of a block; without a counter (one tile a chain) the block's index is its
+// only ticket
+__device__ __forceinline__ Taken first_ticket(unsigned *counter, Taken &shared, unsigned chains, unsigned per_batch) {
+  if (threadIdx.x == 0) hand_out(shared, counter ? atomicAdd(counter, 1u) : blockIdx.x, chains, per_batch);
+  __syncthreads();
+  const Taken t = shared;
+  __syncthreads();  // read before the next one takes its place
+  return t;
 }
 
 }  // namespace ssm

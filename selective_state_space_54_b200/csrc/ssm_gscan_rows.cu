@@ -387,18 +387,30 @@ __device__ __forceinline__ float look_back(const GsParams &p, int64_t row, unsig
   }
   unsigned long long started = 0;
   unsigned n = 0;
-  while (q && w == 0ull) {
-    w = peek(q);
-    if (w == 0ull && !spun(started, n, p.err)) break;
-  }
-  __syncwarp();
-  const float base = __shfl_sync(kAll, of_word((unsigned)w), 31);
-  float h = g > 0 ? base : first;
+  auto wait = [&]() {
+    while (w == 0ull) {
+      w = peek(q);
+      if (w == 0ull && !spun(started, n, p.err)) break;
+    }
+  };
+  // the runs first: they do not wait for anyone's state
+  Run r = no_run();
   if (in > 0) {
-    Run r = lane < in ? of_words(w) : no_run();
+    if (lane < in) {
+      wait();
+      r = of_words(w);
+    }
+    __syncwarp();
     scan_up<ST>(r, lane, 32);
-    h = run_on<ST>(run_of(r, 31, 32), h);
+    r = run_of(r, 31, 32);
   }
+  float h = first;
+  if (g > 0) {
+    if (lane == 31) wait();
+    __syncwarp();
+    h = __shfl_sync(kAll, of_word((unsigned)w), 31);
+  }
+  if (in > 0) h = run_on<ST>(r, h);
   if (lane == 0 && last_in_group && p.group > 1) put_state(p.states + row * p.groups + g, run_on<ST>(tile, h));
   return h;
 }
@@ -407,8 +419,7 @@ constexpr int kTileThreads = 32 * kGsTileWarps;
 
 // A tile of a row: where, and its chunk of this warp
 struct TileShared {
-  unsigned next;
-  Place place;
+  Taken ticket;
   Run run[kGsTileWarps];
   float in[kGsTileWarps], db[kGsTileWarps];
 };
@@ -425,14 +436,9 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
   const Lanes lanes = {32, 0, lane};
   const unsigned chains = (unsigned)(p.batch * p.dim), total = chains * (unsigned)p.tiles;
   const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
-  if (threadIdx.x == 0) {
-    sm.next = atomicAdd(p.ticket, 1u);
-    sm.place = place_of(sm.next, chains, (unsigned)p.dim);
-  }
-  __syncthreads();
-  if (sm.next >= total) return;
-  Place at = sm.place;
-  __syncthreads();  // before the next ticket takes its place
+  const Taken now = first_ticket(p.ticket, sm.ticket, chains, (unsigned)p.dim);
+  if (now.id >= total) return;
+  Place at = now.place;
   fill_stage<T, Z, false>(ring, p, at.chain, ((int64_t)at.time * kGsTileWarps + w) * G::PASS, lanes);
   copies_commit();
   for (int stg = 0;; stg ^= 1) {
@@ -459,16 +465,12 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     scan_up<ST>(r, lane, 32);
     const Run before = run_above(r, 32);
     if (lane == 31) sm.run[w] = r;
-    if (threadIdx.x == 0) {
-      sm.next = drawn;
-      sm.place = place_of(drawn, chains, (unsigned)p.dim);
-    }
+    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, (unsigned)p.dim);
     __syncthreads();
-    const unsigned next_ticket = sm.next;
-    const Place next = sm.place;
-    if (next_ticket < total)
-      fill_stage<T, Z, false>(ring + (stg ^ 1) * kStage<Z, false>, p, next.chain,
-                              ((int64_t)next.time * kGsTileWarps + w) * G::PASS, lanes);
+    const Taken next = sm.ticket;
+    if (next.id < total)
+      fill_stage<T, Z, false>(ring + (stg ^ 1) * kStage<Z, false>, p, next.place.chain,
+                              ((int64_t)next.place.time * kGsTileWarps + w) * G::PASS, lanes);
     copies_commit();
     if (w == 0) {
       float h = look_back<ST, false>(p, row, at.time, p.h0 ? p.h0[row] : 0.f, sm.run, q, seen);
@@ -485,8 +487,8 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     if (p.ckpt && lane == 0 && chunk > 0 && chunk < chunks) p.ckpt[row * chunks + chunk] = hw;
     lane_out<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo, t < p.L);
     __syncwarp();
-    if (next_ticket >= total) break;
-    at = next;
+    if (next.id >= total) break;
+    at = next.place;
   }
 }
 
@@ -652,14 +654,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
   const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
   // the warp's chunk of a tile taken from behind; a tile's chunks past the row's end are empty
   auto chunk_of = [&](unsigned time) { return (int64_t)(p.tiles - 1 - time) * kGsTileWarps + w; };
-  if (threadIdx.x == 0) {
-    sm.next = atomicAdd(p.ticket, 1u);
-    sm.place = place_of(sm.next, chains, (unsigned)p.dim);
-  }
-  __syncthreads();
-  if (sm.next >= total) return;
-  Place at = sm.place;
-  __syncthreads();  // before the next ticket takes its place
+  const Taken now = first_ticket(p.ticket, sm.ticket, chains, (unsigned)p.dim);
+  if (now.id >= total) return;
+  Place at = now.place;
   fill_stage<T, Z, true>(ring, p, at.chain, chunk_of(at.time) * G::PASS, lanes);
   copies_commit();
   for (int stg = 0;; stg ^= 1) {
@@ -690,15 +687,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     const Run before = run_above(r, 32), after = run_below(g, 32);
     const float hin = lane == 0 ? h0 : run_on<ST>(before, h0);
     if (lane == 0) sm.run[w] = g;
-    if (threadIdx.x == 0) {
-      sm.next = drawn;
-      sm.place = place_of(drawn, chains, (unsigned)p.dim);
-    }
+    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, (unsigned)p.dim);
     __syncthreads();
-    const unsigned next_ticket = sm.next;
-    const Place next = sm.place;
-    if (next_ticket < total)
-      fill_stage<T, Z, true>(ring + (stg ^ 1) * kStage<Z, true>, p, next.chain, chunk_of(next.time) * G::PASS, lanes);
+    const Taken next = sm.ticket;
+    if (next.id < total)
+      fill_stage<T, Z, true>(ring + (stg ^ 1) * kStage<Z, true>, p, next.place.chain, chunk_of(next.place.time) * G::PASS,
+                             lanes);
     copies_commit();
     if (w == 0) {
       float P = look_back<ST, true>(p, row, at.time, p.dlast ? p.dlast[row] : 0.f, sm.run, q, seen);
@@ -727,8 +721,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
       }
     }
     __syncwarp();
-    if (next_ticket >= total) break;
-    at = next;
+    if (next.id >= total) break;
+    at = next.place;
   }
 }
 

@@ -18,7 +18,7 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTokThreads = 32 * kTokWarps;
 constexpr int kTokFwdBlocks = 4, kTokBwdBlocks = 3;  // an SM: their shared memory and registers fit
-static_assert(kTokGroup <= 4 * kTokWarps, "a warp waits for four tiles at most");
+static_assert(kTokGroup % (4 * kTokWarps) == 0, "the warps of a block share a group's tiles four at a time");
 
 template <typename T>
 struct Tok {
@@ -164,11 +164,10 @@ __device__ __forceinline__ void cut_at_start(Run2 &r, unsigned st) {
 }
 
 struct TokShared {
-  unsigned next;
-  Place place;
+  Taken ticket;
   f2 A[kTokWarps][32], N[kTokWarps][32], B[kTokWarps][32];  // the warps' runs
   f2 other[kTokWarps][32];                                  // backward: B of the state's runs; sums
-  f2 in[32];                                                // the value entering the tile
+  f2 gA[kTokWarps][32], gN[kTokWarps][32], gB[kTokWarps][32];  // those of the group's earlier tiles
   __device__ __forceinline__ Run2 of(int w, int lane) const { return {A[w][lane], N[w][lane], B[w][lane]}; }
 };
 
@@ -199,54 +198,60 @@ __device__ __forceinline__ const unsigned long long *state_of(const GsParams &p,
 
 // Look-back of the whole block (see the channel-major form): `c` is the tile's index in
 // the direction of the walk, sm holds the warps' runs in that direction (warp 0 first, or
-// last with FROM_BEHIND), `seen` what the lane saw of the group's state when it looked
-// ahead.  Returns the value entering the warp's own run; `out` receives, in the warp that
-// the walk reaches last, the value leaving the tile.  With one tile a group (many chains: the
-// tile before was taken long ago) every warp reads the state itself; else the first warps
-// of the walk gather the runs of the group's tiles (`earlier`), in the order of their index.
+// last with FROM_BEHIND), `q` and `seen` where the group's state is and what the lane saw of
+// it when it looked ahead.  Returns the value entering the warp's own run; `out` receives, in
+// the warp that the walk reaches last, the value leaving the tile.  The runs of the group's
+// earlier tiles are joined in the order of their index, a quarter by each warp, before the
+// state is waited for: from there to the state leaving the tile it is a few steps.
 template <bool ST, bool FROM_BEHIND>
-__device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, unsigned long long (*earlier)[64], int64_t chain,
-                                      unsigned c, f2 first, int w, int lane, const unsigned long long *q, unsigned long long seen, f2 &out) {
+__device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t chain, unsigned c, f2 first, int w,
+                                      int lane, const unsigned long long *q, unsigned long long seen, f2 &out) {
   const unsigned g = c / p.group, in = c - g * p.group;
   const bool last = c == p.tiles - 1, last_in_group = in == p.group - 1;
   const int mine = FROM_BEHIND ? kTokWarps - 1 - w : w;  // the warp's place in the walk
   auto nth = [](int j) { return FROM_BEHIND ? kTokWarps - 1 - j : j; };
-  f2 h = first;
-  if (p.group == 1) {
-    if (q) h = of_pair(wait64(q, seen, p.err));
-  } else {
+  if (p.group > 1) {
     unsigned long long *runs = p.runs + chain * p.tiles * kTokChannels;
-    if (mine == 0) {
-      if (!last && !last_in_group) {
-        Run2 tile = sm.of(nth(0), lane);
+    if (mine == 0 && !last && !last_in_group) {
+      Run2 tile = sm.of(nth(0), lane);
 #pragma unroll
-        for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(nth(j), lane), tile);
-        Run x, y;
-        split(tile, x, y);
-        put_run(runs + (int64_t)c * kTokChannels + 2 * lane, x);
-        put_run(runs + (int64_t)c * kTokChannels + 2 * lane + 1, y);
-      }
-      if (q) h = of_pair(wait64(q, seen, p.err));
+      for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(nth(j), lane), tile);
+      Run x, y;
+      split(tile, x, y);
+      put_run(runs + (int64_t)c * kTokChannels + 2 * lane, x);
+      put_run(runs + (int64_t)c * kTokChannels + 2 * lane + 1, y);
     }
     if (in > 0) {
-      for (unsigned j = mine; j < in; j += kTokWarps) {
-        const unsigned long long *a = runs + ((int64_t)g * p.group + j) * kTokChannels + 2 * lane;
-        earlier[j][2 * lane] = wait64(a, look64(a), p.err);
-        earlier[j][2 * lane + 1] = wait64(a + 1, look64(a + 1), p.err);
+      constexpr unsigned PART = kTokGroup / kTokWarps, AT = 4;  // tiles a warp, and at once
+      Run x = no_run(), y = no_run();
+#pragma unroll 1
+      for (unsigned j0 = mine * PART; j0 < (mine + 1) * PART && j0 < in; j0 += AT) {
+        const unsigned long long *a = runs + ((int64_t)g * p.group + j0) * kTokChannels + 2 * lane;
+        unsigned long long v[AT][2];
+#pragma unroll
+        for (unsigned j = 0; j < AT; ++j) {
+          const bool there = j0 + j < in;
+          v[j][0] = there ? look64(a + j * kTokChannels) : ~0ull;
+          v[j][1] = there ? look64(a + j * kTokChannels + 1) : ~0ull;
+        }
+#pragma unroll
+        for (unsigned j = 0; j < AT; ++j) {
+          if (j0 + j >= in) break;
+          x = join<ST>(of_words(wait64(a + j * kTokChannels, v[j][0], p.err)), x);
+          y = join<ST>(of_words(wait64(a + j * kTokChannels + 1, v[j][1], p.err)), y);
+        }
       }
+      sm.gA[mine][lane] = pack2(x.A, y.A);
+      sm.gN[mine][lane] = pack2(x.N, y.N);
+      sm.gB[mine][lane] = pack2(x.B, y.B);
       __syncthreads();
     }
-    if (mine == 0) {
-      float h0, h1;
-      unpack2(h, h0, h1);
-      for (unsigned j = 0; j < in; ++j) {
-        h0 = run_on<ST>(of_words(earlier[j][2 * lane]), h0);
-        h1 = run_on<ST>(of_words(earlier[j][2 * lane + 1]), h1);
-      }
-      sm.in[lane] = pack2(h0, h1);
-    }
-    __syncthreads();
-    h = sm.in[lane];
+  }
+  f2 h = first;
+  if (q) h = of_pair(wait64(q, seen, p.err));
+  if (in > 0) {
+#pragma unroll
+    for (int j = 0; j < kTokWarps; ++j) h = run_on2<ST>({sm.gA[j][lane], sm.gN[j][lane], sm.gB[j][lane]}, h);
   }
 #pragma unroll
   for (int j = 0; j < kTokWarps - 1; ++j) {
@@ -319,16 +324,10 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
   __shared__ TokShared sm;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned char *ring = smem + w * 2 * STAGE;
-  auto earlier = reinterpret_cast<unsigned long long (*)[64]>(smem + kTokWarps * 2 * STAGE);  // with groups of tiles
   const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
-  if (threadIdx.x == 0) {
-    sm.next = p.ticket ? atomicAdd(p.ticket, 1u) : blockIdx.x;
-    sm.place = place_of(sm.next, chains, cgs);
-  }
-  __syncthreads();
-  if (sm.next >= total) return;
-  Place at = sm.place;
-  __syncthreads();  // before the next ticket takes its place
+  const Taken now = first_ticket(p.ticket, sm.ticket, chains, cgs);
+  if (now.id >= total) return;
+  Place at = now.place;
   fill_stage<T, Z, false>(ring, p, Where<T, false>(p, at, w), lane);
   copies_commit();
   for (int stg = 0;; stg ^= 1) {
@@ -349,17 +348,13 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     sm.A[w][lane] = r.A;
     sm.N[w][lane] = r.N;
     sm.B[w][lane] = r.B;
-    if (threadIdx.x == 0) {
-      sm.next = drawn;
-      sm.place = place_of(drawn, chains, cgs);
-    }
+    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
     __syncthreads();
-    const unsigned next_ticket = sm.next;
-    const Place next = sm.place;
-    if (next_ticket < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next, w), lane);
+    const Taken next = sm.ticket;
+    if (next.id < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next.place, w), lane);
     copies_commit();
     f2 out;
-    f2 h = tile_in<ST, false>(p, sm, earlier, at.chain, at.time, first, w, lane, q, seen, out);
+    f2 h = tile_in<ST, false>(p, sm, at.chain, at.time, first, w, lane, q, seen, out);
     if (p.ckpt && w == 0) store_f32(p.ckpt + ((int64_t)at.batch * p.tiles + at.time) * p.dim, ch, h);
     if (p.last && w == kTokWarps - 1 && at.time == p.tiles - 1) store_f32(p.last + at.batch * p.dim, ch, out);
     if (p.y) {
@@ -383,8 +378,8 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
       if (p.v32 && a.n == RUN) walk(true);
       else walk(false);
     }
-    if (next_ticket >= total) break;
-    at = next;
+    if (next.id >= total) break;
+    at = next.place;
     __syncthreads();  // every warp is done with the tile's runs
   }
 }
@@ -396,16 +391,10 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
   __shared__ TokShared sm;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned char *ring = smem + w * 2 * STAGE;
-  auto earlier = reinterpret_cast<unsigned long long (*)[64]>(smem + kTokWarps * 2 * STAGE);  // with groups of tiles
   const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
-  if (threadIdx.x == 0) {
-    sm.next = p.ticket ? atomicAdd(p.ticket, 1u) : blockIdx.x;
-    sm.place = place_of(sm.next, chains, cgs);
-  }
-  __syncthreads();
-  if (sm.next >= total) return;
-  Place at = sm.place;
-  __syncthreads();  // before the next ticket takes its place
+  const Taken now = first_ticket(p.ticket, sm.ticket, chains, cgs);
+  if (now.id >= total) return;
+  Place at = now.place;
   fill_stage<T, Z, true>(ring, p, Where<T, true>(p, at, w), lane);
   copies_commit();
   for (int stg = 0;; stg ^= 1) {
@@ -445,21 +434,17 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     sm.N[w][lane] = r.N;
     sm.B[w][lane] = R;
     sm.other[w][lane] = r.B;
-    if (threadIdx.x == 0) {
-      sm.next = drawn;
-      sm.place = place_of(drawn, chains, cgs);
-    }
+    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
     __syncthreads();
-    const unsigned next_ticket = sm.next;
-    const Place next = sm.place;
-    if (next_ticket < total) fill_stage<T, Z, true>(ring + (stg ^ 1) * STAGE, p, Where<T, true>(p, next, w), lane);
+    const Taken next = sm.ticket;
+    if (next.id < total) fill_stage<T, Z, true>(ring + (stg ^ 1) * STAGE, p, Where<T, true>(p, next.place, w), lane);
     copies_commit();
 #pragma unroll
     for (int i = 0; i < kTokWarps - 1; ++i) {
       if (i < w) h = run_on2<ST>({sm.A[i][lane], sm.N[i][lane], sm.other[i][lane]}, h);
     }
     f2 out;
-    f2 P = tile_in<ST, true>(p, sm, earlier, at.chain, at.time, first, w, lane, q, seen, out);
+    f2 P = tile_in<ST, true>(p, sm, at.chain, at.time, first, w, lane, q, seen, out);
     if (p.dh0 && w == 0 && a.time == 0) store_f32(p.dh0 + at.batch * p.dim, ch, out);
     f2 sum = splat2(0.f);
     auto walk = [&](bool all) {
@@ -511,8 +496,8 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
         store_f32(p.dbias_part + ((int64_t)at.batch * p.tiles + a.time) * p.dim, ch, t);
       }
     }
-    if (next_ticket >= total) break;
-    at = next;
+    if (next.id >= total) break;
+    at = next.place;
     if (p.dbias_part) __syncthreads();
   }
 }
@@ -520,8 +505,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
 template <typename T, bool TIED, bool Z, bool ST>
 cudaError_t launch_t(bool bwd, const GsParams &p, cudaStream_t s) {
   const int64_t n = p.batch * gs_tok_groups(p.dim) * p.tiles;
-  const int smem = kTokWarps * 2 * (bwd ? kWarpStage<Z, true> : kWarpStage<Z, false>) +
-                   (p.group > 1 ? kTokGroup * 64 * (int)sizeof(unsigned long long) : 0);
+  const int smem = kTokWarps * 2 * (bwd ? kWarpStage<Z, true> : kWarpStage<Z, false>);
   auto kern = bwd ? k_tok_bwd<T, TIED, Z, ST> : k_tok_fwd<T, TIED, Z, ST>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

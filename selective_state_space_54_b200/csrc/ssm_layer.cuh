@@ -27,7 +27,7 @@ constexpr int kGsRowGroup = 31;    // tiles between two published states of a ro
 // run a quarter of it.  Saved [batch][tile][dim] fp32, the state entering every tile.
 constexpr int kTokChannels = 64;
 constexpr int kTokWarps = 4;
-constexpr int kTokGroup = 16;      // tiles between two published states of a channel, at most
+constexpr int kTokGroup = 32;      // tiles between two published states of a channel, at most
 __host__ __device__ constexpr int gs_tok_steps(int esize) { return 128 / esize; }
 __host__ __device__ __forceinline__ int64_t gs_tok_tiles(int64_t L, int esize) {
   return (L + gs_tok_steps(esize) - 1) / gs_tok_steps(esize);
