@@ -308,31 +308,56 @@ def scan_bwd(u, delta, A, B, C, D, z, delta_bias, dout, *, delta_softplus=True,
 
 
 # ---- gated linear recurrence and layer norm ------------------------------------
+# The host's share of a call decides the smallest ones (a decode step's kernel takes 2 us),
+# so the common path is kept short: one combined test per tensor, addresses passed as plain
+# integers, the stream's handle without a Stream object.
 class _launch:
-    """The stream a call launches on, as ``with _launch(device, stream) as handle:``:
-    the caller's, or the current one of the tensors' own device.  The device is made
-    current for the launch, and what the call allocates belongs to that stream."""
-    __slots__ = ("device", "stream", "guards")
+    """``with _launch(device, stream) as handle:`` makes the caller's stream, or the tensors'
+    own device, current for a launch; what the call allocates belongs to that stream."""
+    __slots__ = ("device", "stream", "guard")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, None
+        self.device, self.stream, self.guard = device, stream, None
 
     def __enter__(self):
         import torch
         if self.stream is None:
-            if torch.cuda.current_device() != self.device.index:
-                self.guards = torch.cuda.device(self.device)
-                self.guards.__enter__()
-            return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-        if self.stream.device != self.device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
-        self.guards = torch.cuda.stream(self.stream)
-        self.guards.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+            self.guard = torch.cuda.device(self.device)
+        else:
+            if self.stream.device != self.device:
+                raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
+            self.guard = torch.cuda.stream(self.stream)
+        self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
 
     def __exit__(self, *exc):
-        if self.guards is not None:
-            self.guards.__exit__(*exc)
+        self.guard.__exit__(*exc)
+
+
+_raw_stream = None
+
+
+def _on_stream(device, stream, call):
+    """call(handle) with the launch's stream and device current."""
+    global _raw_stream
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda index: torch.cuda.current_stream(index).cuda_stream)
+        return call(_raw_stream(device.index))
+    with _launch(device, stream) as handle:
+        return call(handle)
+
+
+def _fits(t, shape, dtype, index):
+    # index: the CUDA device's (a CPU tensor has -1)
+    return t is None or (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _cuda_device(name, t):
@@ -359,6 +384,11 @@ def _workspace_for(nbytes, device, workspace):
 def _gated_shape(batch, dim, seqlen, io_dtype, path, flags):
     # read-only for the library (a const pointer): one struct serves every call of a shape
     return make_shape(batch, dim, seqlen, 1, io_dtype, path, flags=flags)
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_step_ref(batch, dim, io_dtype, flags):
+    return ctypes.byref(_gated_shape(batch, dim, 1, io_dtype, SSM_PATH_AUTO, flags))
 
 
 def gated_scan_shape(u, *, tied=True, save_states=False, token_major=False, path: int = SSM_PATH_AUTO) -> ssm_shape:
@@ -393,17 +423,19 @@ def _check_starts(starts, batch, seqlen, dev):
     return starts
 
 
-def _check_gated(shape, u, f, z, f_bias, starts, initial_state, token_major):
+def _check_gated(shape, u, f, z, f_bias, starts, initial_state):
     import torch
-    batch, dim, seqlen = shape.batch, shape.dim, shape.seqlen
-    dt, dev = u.dtype, u.device
-    act = u.shape
+    batch, dim, dt, dev, f32 = shape.batch, shape.dim, u.dtype, u.device, torch.float32
+    act, per, states, at = u.shape, (dim,), (batch, dim), u.get_device()
+    if (starts is None and u.is_contiguous() and _fits(f, act, dt, at) and _fits(z, act, dt, at)
+            and _fits(f_bias, per, f32, at) and _fits(initial_state, states, f32, at)):
+        return
     _check_io("u", u, act, dt, dev)
     _check_io("f", f, act, dt, dev)
     _check_io("z", z, act, dt, dev)
-    _check_io("f_bias", f_bias, (dim,), torch.float32, dev)
-    _check_io("initial_state", initial_state, (batch, dim), torch.float32, dev)
-    _check_starts(starts, batch, seqlen, dev)
+    _check_io("f_bias", f_bias, per, f32, dev)
+    _check_io("initial_state", initial_state, states, f32, dev)
+    _check_starts(starts, batch, shape.seqlen, dev)
 
 
 def gated_scan_fwd(u, f, z=None, f_bias=None, *, tied=True, starts=None, initial_state=None, y=None,
@@ -417,35 +449,39 @@ def gated_scan_fwd(u, f, z=None, f_bias=None, *, tied=True, starts=None, initial
     (dim,) and the states (batch, dim) fp32.  starts (batch, seqlen), bool or uint8: a
     packed sequence starts there, so h_{t-1} counts as 0 (initial_state too, at t = 0).
     save_states writes the states gated_scan_bwd(fwd_workspace=...) needs into
-    ``workspace`` (which must then be given).  check_status: as in scan_fwd."""
+    ``workspace`` (which must then be given).  check_status: as in scan_fwd.  The call runs
+    on the tensors' device, on ``stream`` or that device's current one."""
     import torch
     dev = _cuda_device("u", u)
     shape = gated_scan_shape(u, tied=tied, save_states=save_states, token_major=token_major, path=path)
-    _check_gated(shape, u, f, z, f_bias, starts, initial_state, token_major)
+    _check_gated(shape, u, f, z, f_bias, starts, initial_state)
     if save_states and workspace is None:
         raise ValueError("save_states writes into the workspace: pass workspace=")
+    states = (shape.batch, shape.dim)
+    if y is not None:
+        _check_io("y", y, u.shape, u.dtype, dev)
+    if last_state is not None:
+        _check_io("last_state", last_state, states, torch.float32, dev)
     lib = _lib.load()
     ref = ctypes.byref(shape)
-    with _launch(dev, stream) as handle:
-        if y is None:
-            y = torch.empty_like(u)
-        else:
-            _check_io("y", y, u.shape, u.dtype, dev)
-        if last_state is not None:
-            _check_io("last_state", last_state, (shape.batch, shape.dim), torch.float32, dev)
-        elif return_last_state:
-            last_state = torch.empty((shape.batch, shape.dim), dtype=torch.float32, device=dev)
-        nbytes = int(lib.ssm_gated_scan_fwd_workspace_bytes(ref))
+
+    def call(handle):
+        out = torch.empty_like(u) if y is None else y
+        last = last_state
+        if last is None and return_last_state:
+            last = torch.empty(states, dtype=torch.float32, device=dev)
+        nbytes = lib.ssm_gated_scan_fwd_workspace_bytes(ref)
         ws = _workspace_for(nbytes, dev, workspace)
-        rc = lib.ssm_gated_scan_fwd(ref, _ptr(u), _ptr(f), _ptr(z), _ptr(f_bias), _ptr(starts), _ptr(initial_state),
-                                    _ptr(y), _ptr(last_state), _ptr(ws), 0 if ws is None else ws.nbytes, handle)
+        rc = lib.ssm_gated_scan_fwd(ref, u.data_ptr(), f.data_ptr(), _addr(z), _addr(f_bias), _addr(starts),
+                                    _addr(initial_state), out.data_ptr(), _addr(last), _addr(ws),
+                                    0 if ws is None else ws.nbytes, handle)
         if rc != 0:
             raise ScanError(rc, "ssm_gated_scan_fwd")
         if check_status and nbytes:
             check(ws, stream)
-    if return_last_state:
-        return y, last_state
-    return y
+        return (out, last) if return_last_state else out
+
+    return _on_stream(dev, stream, call)
 
 
 def gated_scan_bwd(u, f, z, f_bias, dout, *, tied=True, starts=None, initial_state=None, dlast_state=None,
@@ -454,37 +490,43 @@ def gated_scan_bwd(u, f, z, f_bias, dout, *, tied=True, starts=None, initial_sta
     """Backward of gated_scan_fwd by recomputation; returns a dict of the gradients
     du, df, dz, df_bias, dinitial_state (None for what is absent).  dlast_state
     (batch, dim) fp32: the gradient reaching last_state.  fwd_workspace: the workspace
-    of a gated_scan_fwd(save_states=True) call on the same inputs."""
+    of a gated_scan_fwd(save_states=True) call on the same inputs, with the same ``path``."""
     import torch
     dev = _cuda_device("u", u)
     shape = gated_scan_shape(u, tied=tied, save_states=fwd_workspace is not None, token_major=token_major, path=path)
-    _check_gated(shape, u, f, z, f_bias, starts, initial_state, token_major)
-    batch, dim, f32 = shape.batch, shape.dim, torch.float32
+    _check_gated(shape, u, f, z, f_bias, starts, initial_state)
+    f32, states, per = torch.float32, (shape.batch, shape.dim), (shape.dim,)
     _check_io("dout", dout, u.shape, u.dtype, dev)
-    _check_io("dlast_state", dlast_state, (batch, dim), f32, dev)
+    _check_io("dlast_state", dlast_state, states, f32, dev)
     lib = _lib.load()
     ref = ctypes.byref(shape)
-    if fwd_workspace is not None:
-        _workspace_for(int(lib.ssm_gated_scan_fwd_workspace_bytes(ref)), dev, fwd_workspace)
-    with _launch(dev, stream) as handle:
-        g = dict(out or {})
-        for k, like, shp, ty in (("du", u, u.shape, u.dtype), ("df", u, u.shape, u.dtype), ("dz", z, u.shape, u.dtype),
-                                 ("df_bias", f_bias, (dim,), f32),
-                                 ("dinitial_state", u if want_dinitial_state else None, (batch, dim), f32)):
-            if g.get(k) is not None:
-                _check_io(k, g[k], shp, ty, dev)
-            else:
-                g[k] = torch.empty(shp, dtype=ty, device=dev) if like is not None else None
-        ws = _workspace_for(int(lib.ssm_gated_scan_bwd_workspace_bytes(ref)), dev, workspace)
+    given = out or {}
+
+    def gradient(name, like, shp, ty):
+        if given.get(name) is not None:
+            _check_io(name, given[name], shp, ty, dev)
+            return given[name]
+        return None if like is None else torch.empty(shp, dtype=ty, device=dev)
+
+    def call(handle):
+        if fwd_workspace is not None:
+            _workspace_for(lib.ssm_gated_scan_fwd_workspace_bytes(ref), dev, fwd_workspace)
+        g = {"du": gradient("du", u, u.shape, u.dtype), "df": gradient("df", u, u.shape, u.dtype),
+             "dz": gradient("dz", z, u.shape, u.dtype), "df_bias": gradient("df_bias", f_bias, per, f32),
+             "dinitial_state": gradient("dinitial_state", u if want_dinitial_state else None, states, f32)}
+        ws = _workspace_for(lib.ssm_gated_scan_bwd_workspace_bytes(ref), dev, workspace)
         rc = lib.ssm_gated_scan_bwd(
-            ref, _ptr(u), _ptr(f), _ptr(z), _ptr(f_bias), _ptr(starts), _ptr(initial_state), _ptr(dout),
-            _ptr(dlast_state), _ptr(fwd_workspace), _ptr(g["du"]), _ptr(g["df"]), _ptr(g["dz"]), _ptr(g["df_bias"]),
-            _ptr(g["dinitial_state"]), _ptr(ws), 0 if ws is None else ws.nbytes, handle)
+            ref, u.data_ptr(), f.data_ptr(), _addr(z), _addr(f_bias), _addr(starts), _addr(initial_state),
+            dout.data_ptr(), _addr(dlast_state), _addr(fwd_workspace), g["du"].data_ptr(), g["df"].data_ptr(),
+            _addr(g["dz"]), _addr(g["df_bias"]), _addr(g["dinitial_state"]), _addr(ws),
+            0 if ws is None else ws.nbytes, handle)
         if rc != 0:
             raise ScanError(rc, "ssm_gated_scan_bwd")
         if check_status and ws is not None:
             check(ws, stream)
-    return g
+        return g
+
+    return _on_stream(dev, stream, call)
 
 
 def gated_scan_step(u, f, z=None, f_bias=None, *, state, tied=True, y=None, stream=None):
@@ -492,24 +534,24 @@ def gated_scan_step(u, f, z=None, f_bias=None, *, state, tied=True, y=None, stre
     (batch, dim) fp32 in place and returns y.  u, f, z, y (batch, dim)."""
     import torch
     dev = _cuda_device("u", u)
-    batch, dim = u.shape
-    dt = u.dtype
-    _check_io("u", u, (batch, dim), dt, dev)
-    _check_io("f", f, (batch, dim), dt, dev)
-    _check_io("z", z, (batch, dim), dt, dev)
-    _check_io("f_bias", f_bias, (dim,), torch.float32, dev)
-    _check_io("state", state, (batch, dim), torch.float32, dev)
-    shape = _gated_shape(batch, dim, 1, _io_dtype(u), SSM_PATH_AUTO, 0 if tied else SSM_FLAG_UNTIED)
-    with _launch(dev, stream) as handle:
-        if y is None:
-            y = torch.empty_like(u)
-        else:
-            _check_io("y", y, (batch, dim), dt, dev)
-        rc = _lib.load().ssm_gated_scan_step(ctypes.byref(shape), _ptr(u), _ptr(f), _ptr(z), _ptr(f_bias),
-                                             _ptr(state), _ptr(y), handle)
-    if rc != 0:
-        raise ScanError(rc, "ssm_gated_scan_step")
-    return y
+    act, dt, f32, at = u.shape, u.dtype, torch.float32, u.get_device()
+    batch, dim = act
+    if not (u.is_contiguous() and _fits(f, act, dt, at) and _fits(z, act, dt, at) and _fits(y, act, dt, at)
+            and _fits(f_bias, (dim,), f32, at) and _fits(state, act, f32, at)):
+        for name, t, shp, ty in (("u", u, act, dt), ("f", f, act, dt), ("z", z, act, dt), ("y", y, act, dt),
+                                 ("f_bias", f_bias, (dim,), f32), ("state", state, act, f32)):
+            _check_io(name, t, shp, ty, dev)
+    ref = _gated_step_ref(batch, dim, _io_dtype(u), 0 if tied else SSM_FLAG_UNTIED)
+
+    def call(handle):
+        out = torch.empty_like(u) if y is None else y
+        rc = _lib.load().ssm_gated_scan_step(ref, u.data_ptr(), f.data_ptr(), _addr(z), _addr(f_bias),
+                                             state.data_ptr(), out.data_ptr(), handle)
+        if rc != 0:
+            raise ScanError(rc, "ssm_gated_scan_step")
+        return out
+
+    return _on_stream(dev, stream, call)
 
 
 def _residual_dtype(name, t, io) -> int:
@@ -530,32 +572,35 @@ def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, residua
     dev = _cuda_device("x", x)
     if x.dim() < 1:
         raise ValueError("x needs at least one axis")
-    dt, dim = x.dtype, x.shape[-1]
+    act, dt, f32 = x.shape, x.dtype, torch.float32
+    dim = act[-1]
     rows = x.numel() // dim if dim else 0
     io = rd = _io_dtype(x)
-    _check_io("x", x, x.shape, dt, dev)
-    _check_io("weight", weight, (dim,), torch.float32, dev)
-    _check_io("bias", bias, (dim,), torch.float32, dev)
+    rt = dt
     if residual is not None:
-        rd = _residual_dtype("residual", residual, dt)
-        _check_io("residual", residual, x.shape, residual.dtype, dev)
+        rd, rt = _residual_dtype("residual", residual, dt), residual.dtype
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    with _launch(dev, stream) as handle:
-        if y is None:
-            y = torch.empty_like(x)
-        else:
-            _check_io("y", y, x.shape, dt, dev)
-        if residual is not None:
-            if residual_out is None:
-                residual_out = torch.empty_like(residual)
-            else:
-                _check_io("residual_out", residual_out, x.shape, residual.dtype, dev)
-        rc = _lib.load().ssm_layer_norm(rows, dim, io, rd, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps,
-                                        _ptr(y), _ptr(residual_out), handle)
-    if rc != 0:
-        raise ScanError(rc, "ssm_layer_norm")
-    return y if residual is None else (y, residual_out)
+    at = x.get_device()
+    if not (x.is_contiguous() and _fits(weight, (dim,), f32, at) and _fits(bias, (dim,), f32, at)
+            and _fits(residual, act, rt, at) and _fits(y, act, dt, at) and _fits(residual_out, act, rt, at)):
+        for name, t, shp, ty in (("x", x, act, dt), ("weight", weight, (dim,), f32), ("bias", bias, (dim,), f32),
+                                 ("residual", residual, act, rt), ("y", y, act, dt),
+                                 ("residual_out", residual_out, act, rt)):
+            _check_io(name, t, shp, ty, dev)
+
+    def call(handle):
+        out = torch.empty_like(x) if y is None else y
+        total = residual_out
+        if total is None and residual is not None:
+            total = torch.empty_like(residual)
+        rc = _lib.load().ssm_layer_norm(rows, dim, io, rd, x.data_ptr(), _addr(residual), weight.data_ptr(),
+                                        _addr(bias), eps, out.data_ptr(), _addr(total), handle)
+        if rc != 0:
+            raise ScanError(rc, "ssm_layer_norm")
+        return out if residual is None else (out, total)
+
+    return _on_stream(dev, stream, call)
 
 
 def layer_norm_bwd_workspace_bytes(rows: int, dim: int) -> int:
@@ -574,35 +619,37 @@ def layer_norm_bwd(s, weight, bias, dy, *, eps=1e-5, dresidual_out=None, out=Non
     dev = _cuda_device("dy", dy)
     if dy.dim() < 1:
         raise ValueError("dy needs at least one axis")
-    dt, dim, f32 = dy.dtype, dy.shape[-1], torch.float32
+    act, dt, f32 = dy.shape, dy.dtype, torch.float32
+    dim = act[-1]
     rows = dy.numel() // dim if dim else 0
-    io = _io_dtype(dy)
-    rd = _residual_dtype("s", s, dt)
-    _check_io("s", s, dy.shape, s.dtype, dev)
-    _check_io("dy", dy, dy.shape, dt, dev)
-    _check_io("weight", weight, (dim,), f32, dev)
-    _check_io("bias", bias, (dim,), f32, dev)
-    _check_io("dresidual_out", dresidual_out, dy.shape, s.dtype, dev)
+    io, rd, rt = _io_dtype(dy), _residual_dtype("s", s, dt), s.dtype
+    for name, t, shp, ty in (("s", s, act, rt), ("dy", dy, act, dt), ("weight", weight, (dim,), f32),
+                             ("bias", bias, (dim,), f32), ("dresidual_out", dresidual_out, act, rt)):
+        _check_io(name, t, shp, ty, dev)
     lib = _lib.load()
-    with _launch(dev, stream) as handle:
-        g = dict(out or {})
-        for k, want, shp, ty in (("dx", True, dy.shape, dt), ("dresidual", io != rd, dy.shape, s.dtype),
-                                 ("dweight", True, (dim,), f32), ("dbias", bias is not None, (dim,), f32)):
-            if not want:
-                g[k] = None
-            elif g.get(k) is not None:
-                _check_io(k, g[k], shp, ty, dev)
-            else:
-                g[k] = torch.empty(shp, dtype=ty, device=dev)
-        ws = _workspace_for(int(lib.ssm_layer_norm_bwd_workspace_bytes(rows, dim)), dev, workspace)
-        rc = lib.ssm_layer_norm_bwd(rows, dim, io, rd, _ptr(s), _ptr(weight), eps, _ptr(dy), _ptr(dresidual_out),
-                                    _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
-                                    _ptr(ws), 0 if ws is None else ws.nbytes, handle)
-    if rc != 0:
-        raise ScanError(rc, "ssm_layer_norm_bwd")
-    if io == rd:
-        g["dresidual"] = g["dx"]
-    return g
+    given = out or {}
+
+    def gradient(name, wanted, shp, ty):
+        if wanted and given.get(name) is not None:
+            _check_io(name, given[name], shp, ty, dev)
+            return given[name]
+        return torch.empty(shp, dtype=ty, device=dev) if wanted else None
+
+    def call(handle):
+        g = {"dx": gradient("dx", True, act, dt), "dresidual": gradient("dresidual", io != rd, act, rt),
+             "dweight": gradient("dweight", True, (dim,), f32), "dbias": gradient("dbias", bias is not None, (dim,), f32)}
+        ws = _workspace_for(lib.ssm_layer_norm_bwd_workspace_bytes(rows, dim), dev, workspace)
+        rc = lib.ssm_layer_norm_bwd(rows, dim, io, rd, s.data_ptr(), weight.data_ptr(), eps, dy.data_ptr(),
+                                    _addr(dresidual_out), g["dx"].data_ptr(), _addr(g["dresidual"]),
+                                    g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(ws),
+                                    0 if ws is None else ws.nbytes, handle)
+        if rc != 0:
+            raise ScanError(rc, "ssm_layer_norm_bwd")
+        if io == rd:
+            g["dresidual"] = g["dx"]
+        return g
+
+    return _on_stream(dev, stream, call)
 
 
 def check(workspace, stream=None) -> None:
