@@ -18,7 +18,6 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTokThreads = 32 * kTokWarps;
 constexpr int kTokFwdBlocks = 4, kTokBwdBlocks = 3;  // an SM: their shared memory and registers fit
-static_assert(kTokGroup % (4 * kTokWarps) == 0, "the warps of a block share a group's tiles four at a time");
 
 template <typename T>
 struct Tok {
@@ -222,21 +221,22 @@ __device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t 
       put_run(runs + (int64_t)c * kTokChannels + 2 * lane + 1, y);
     }
     if (in > 0) {
-      constexpr unsigned PART = kTokGroup / kTokWarps, AT = 4;  // tiles a warp, and at once
+      constexpr unsigned AT = 4;  // words of tiles on their way at once
+      const unsigned part = (p.group + kTokWarps - 1) / kTokWarps, end = min(in, (mine + 1) * part);
       Run x = no_run(), y = no_run();
 #pragma unroll 1
-      for (unsigned j0 = mine * PART; j0 < (mine + 1) * PART && j0 < in; j0 += AT) {
+      for (unsigned j0 = mine * part; j0 < end; j0 += AT) {
         const unsigned long long *a = runs + ((int64_t)g * p.group + j0) * kTokChannels + 2 * lane;
         unsigned long long v[AT][2];
 #pragma unroll
         for (unsigned j = 0; j < AT; ++j) {
-          const bool there = j0 + j < in;
+          const bool there = j0 + j < end;
           v[j][0] = there ? look64(a + j * kTokChannels) : ~0ull;
           v[j][1] = there ? look64(a + j * kTokChannels + 1) : ~0ull;
         }
 #pragma unroll
         for (unsigned j = 0; j < AT; ++j) {
-          if (j0 + j >= in) break;
+          if (j0 + j >= end) break;
           x = join<ST>(of_words(wait64(a + j * kTokChannels, v[j][0], p.err)), x);
           y = join<ST>(of_words(wait64(a + j * kTokChannels + 1, v[j][1], p.err)), y);
         }

@@ -3,6 +3,7 @@
 // the public contract is include/ssm_scan.h.
 #include <string.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -54,7 +55,7 @@ struct GsPlan {
 // (each holds two passes of its row in flight); with fewer, rows longer than one tile
 // are split into tiles.
 constexpr int64_t kRowsPerSm = 8;
-constexpr int64_t kTilesPerSm = 3;  // tiles an SM works on at once
+constexpr int64_t kGroupChains = 512;
 
 ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   GsPlan l;
@@ -73,10 +74,12 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   const int64_t width = tok ? kTokChannels : 1;
   if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L, es) : (L + row_tile - 1) / row_tile;
   if ((double)chains * (double)l.tiles > 2.0e9) return SSM_ERR_UNSUPPORTED;  // a grid dimension
-  // Tiles between two published states: one where there are more chains than tiles at work
-  // (the tile before was taken a whole round ago: its state is there), else many, so that a
-  // chain's state takes few steps from tile to tile.
-  if (chains < kTilesPerSm * (int64_t)l.sms) l.group = tok ? kTokGroup : kGsRowGroup;
+  // Tiles between two published states (a group): a chain's state takes some 1.2 us from
+  // one published state to the next, while HBM moves a tile of every chain (32 KB each,
+  // forward) in 5 ns a chain, so about 240 / chains tiles a group keep up; three times as
+  // many leave room, and more only add work.
+  if (l.path == SSM_PATH_LOOKBACK)
+    l.group = std::min<int64_t>(tok ? kTokGroup : kGsRowGroup, (kGroupChains + chains - 1) / chains);
   l.groups = (l.tiles + l.group - 1) / l.group;
   l.part_rows = s->batch * (l.path == SSM_PATH_LOOKBACK ? l.tiles : 1);
   const bool save = bwd || (s->flags & SSM_FLAG_SAVE_STATES);
