@@ -55,7 +55,6 @@ struct GsPlan {
 // (each holds two passes of its row in flight); with fewer, rows longer than one tile
 // are split into tiles.
 constexpr int64_t kRowsPerSm = 8;
-constexpr int64_t kGroupChains = 512;
 
 ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   GsPlan l;
@@ -74,12 +73,15 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   const int64_t width = tok ? kTokChannels : 1;
   if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L, es) : (L + row_tile - 1) / row_tile;
   if ((double)chains * (double)l.tiles > 2.0e9) return SSM_ERR_UNSUPPORTED;  // a grid dimension
-  // Tiles between two published states (a group): a chain's state takes some 1.2 us from
-  // one published state to the next, while HBM moves a tile of every chain (32 KB each,
-  // forward) in 5 ns a chain, so about 240 / chains tiles a group keep up; three times as
-  // many leave room, and more only add work.
-  if (l.path == SSM_PATH_LOOKBACK)
-    l.group = std::min<int64_t>(tok ? kTokGroup : kGsRowGroup, (kGroupChains + chains - 1) / chains);
+  // Tiles between two published states (a group).  One where there are enough chains: a
+  // chain's state then takes about 1.2 us from tile to tile, which the tiles of the other
+  // chains fill.  With fewer the chain itself would set the pace, and the tiles of a group
+  // hand on their runs first (a state every group), which costs each tile a look at all of
+  // them.  Measured forward, bf16: channel-major 64 x 262144 75 us with single tiles, 90 us
+  // with groups of 31; token-major 64 chains (4096 channels x 32768) 407 and 311 us (groups
+  // of 8), 128 chains equal, 4 chains (256 x 65536) 643 and 72 us (groups of 32).
+  if (l.path == SSM_PATH_LOOKBACK && chains < (tok ? 96 : 48))
+    l.group = std::min<int64_t>(tok ? kTokGroup : kGsRowGroup, (512 + chains - 1) / chains);
   l.groups = (l.tiles + l.group - 1) / l.group;
   l.part_rows = s->batch * (l.path == SSM_PATH_LOOKBACK ? l.tiles : 1);
   const bool save = bwd || (s->flags & SSM_FLAG_SAVE_STATES);
