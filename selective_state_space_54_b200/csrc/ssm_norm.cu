@@ -251,55 +251,63 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
   }
 }
 
-// rows without 16-byte accesses: NV columns per thread, one row (or several) per block
-template <typename T, typename R, int NV>
-__global__ void __launch_bounds__(512, 1) k_norm(NormParams p, int wpr) {
+// Rows without such accesses: NV single columns per thread, a warp's 32 lanes side by side;
+// otherwise as above, one row at a time.
+template <typename T, typename R, bool RES, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_norm_elems(NormParams p, int wpr) {
   __shared__ RowSums red[2];
-  const int tpr = 32 * wpr, rpb = blockDim.x / tpr, tid = threadIdx.x & (tpr - 1), dim = (int)p.dim;
-  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, base = row * p.dim;
-  const bool live = row < p.rows;  // the last block's spare threads only keep the barriers company
+  const int tpr = 32 * wpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
+  const int dim = (int)p.dim;
+  const float inv = 1.f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  T x[NV];
+  R a[RES ? NV : 1];
+  auto load = [&](int64_t r) {
+    const int64_t base = r * p.dim + tid;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      x[k] = T(0);
+      if constexpr (RES) a[k] = R(0);
+      if (r < p.rows && k * tpr + tid < dim) {
+        x[k] = static_cast<const T *>(p.x)[base + k * tpr];
+        if constexpr (RES) a[k] = static_cast<const R *>(p.res)[base + k * tpr];
+      }
+    }
+  };
+  load(row);
   clear(red[0]);
   clear(red[1]);
   __syncthreads();
-  const T *x = static_cast<const T *>(p.x) + base;
-  float v[NV], sum[1] = {0.f}, sq[1] = {0.f};
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, row += step) {
+    const bool live = row < p.rows;
+    const int64_t base = row * p.dim + tid;
+    float v[NV], sum[1] = {0.f}, sq[1] = {0.f};
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = k * tpr + tid;
-    v[k] = live && i < dim ? IO<T>::get(x, i) : 0.f;
-  }
-  if (p.res) {
-    const R *res = static_cast<const R *>(p.res) + base;
-    float a[NV];
+    for (int k = 0; k < NV; ++k) {
+      v[k] = IO<T>::get(&x[k], 0);
+      if constexpr (RES) {
+        v[k] = stored<R>(v[k] + IO<R>::get(&a[k], 0));
+        if (live && k * tpr + tid < dim) IO<R>::store1(static_cast<R *>(p.res_out), base + k * tpr, v[k]);
+      }
+      sum[0] += v[k];
+    }
+    load(row + step);
+    row_sums<1>(sum, wpr, group, red[0]);
+    const float m = sum[0] * inv;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      v[k] -= m;
+      if (k * tpr + tid < dim) sq[0] = fmaf(v[k], v[k], sq[0]);
+    }
+    row_sums<1>(sq, wpr, group, red[1]);
+    const float r = rsqrtf(fmaf(sq[0], inv, p.eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = k * tpr + tid;
-      a[k] = live && i < dim ? IO<R>::get(res, i) : 0.f;
+      if (live && i < dim)
+        IO<T>::store1(static_cast<T *>(p.y), base + k * tpr, fmaf(v[k] * r, __ldg(p.w + i), p.b ? __ldg(p.b + i) : 0.f));
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = k * tpr + tid;
-      v[k] = stored<R>(v[k] + a[k]);
-      if (live && i < dim) IO<R>::store1(static_cast<R *>(p.res_out) + base, i, v[k]);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < NV; ++k) sum[0] += v[k];
-  row_sums<1>(sum, wpr, threadIdx.x / tpr, red[0]);
-  const float m = sum[0] / (float)dim;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    v[k] -= m;
-    if (k * tpr + tid < dim) sq[0] = fmaf(v[k], v[k], sq[0]);
-  }
-  row_sums<1>(sq, wpr, threadIdx.x / tpr, red[1]);
-  if (!live) return;
-  const float r = 1.f / sqrtf(sq[0] / (float)dim + p.eps);
-  T *y = static_cast<T *>(p.y) + base;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = k * tpr + tid;
-    if (i < dim) IO<T>::store1(y, i, p.b ? fmaf(v[k] * r, p.w[i], p.b[i]) : v[k] * r * p.w[i]);
   }
 }
 
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
   const float inv = 1.f / (float)dim;
   const int64_t step = (int64_t)gridDim.x * groups;
   int64_t row = (int64_t)blockIdx.x * groups + group;
-  Raw8<R> s[NV];
+  Raw8<R> s[NV], dro[DRO ? NV : 1];
   Raw8<T> d[NV];
   auto load = [&](int64_t r) {
 #pragma unroll
@@ -401,6 +409,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
       if (r < p.rows && i < dim) {
         load8<R>(s[k], static_cast<const R *>(p.s) + r * p.dim + i);
         load8<T>(d[k], static_cast<const T *>(p.dy) + r * p.dim + i);
+        if constexpr (DRO) load8<R>(dro[k], static_cast<const R *>(p.dres_out) + r * p.dim + i);
       }
     }
   };
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
     for (int k = 0; k < NV; ++k) {
       const int i = (k * tpr + tid) * 8;
       if (!live || i >= dim) continue;
-      if constexpr (DRO) load8<R>(o[k], static_cast<const R *>(p.dres_out) + row * p.dim + i);
+      if constexpr (DRO) o[k] = dro[k];
       g[k] = d[k];
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[k][e] = pair_of<R>(s[k], e);
@@ -488,41 +497,63 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
   }
 }
 
-// rows without 16-byte accesses: NV columns per thread, in registers
-template <typename T, typename R, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NV <= 4 ? 3 : 2) k_norm_bwd(NormBwdParams p, int wpr) {
+// rows without 16-byte accesses: NV single columns per thread
+template <typename T, typename R, bool DRO, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_elems(NormBwdParams p, int wpr) {
   __shared__ RowSums red[2];
-  __shared__ float acc[THREADS];
-  const int tpr = 32 * wpr, rpb = THREADS / tpr, tid = threadIdx.x & (tpr - 1), dim = (int)p.dim;
-  const float n = (float)dim;
+  __shared__ float acc[MAXT];
+  const int tpr = 32 * wpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
+  const int dim = (int)p.dim;
+  const float inv = 1.f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  R s[NV];
+  T d[NV];
+  auto load = [&](int64_t r) {
+    const int64_t base = r * p.dim + tid;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      s[k] = R(0);
+      d[k] = T(0);
+      if (r < p.rows && k * tpr + tid < dim) {
+        s[k] = static_cast<const R *>(p.s)[base + k * tpr];
+        d[k] = static_cast<const T *>(p.dy)[base + k * tpr];
+      }
+    }
+  };
+  load(row);
   float dw[NV], db[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) dw[k] = db[k] = 0.f;
   clear(red[0]);
   clear(red[1]);
   __syncthreads();
-  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.rows; r0 += (int64_t)gridDim.x * rpb) {
-    const int64_t row = r0 + threadIdx.x / tpr, base = row * p.dim;
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, row += step) {
     const bool live = row < p.rows;
+    const int64_t base = row * p.dim + tid;
     float c[NV], g[NV], sum[1] = {0.f}, s3[3] = {0.f, 0.f, 0.f};
+    R o[DRO ? NV : 1];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = k * tpr + tid;
-      const bool in = live && i < dim;
-      c[k] = in ? IO<R>::get(static_cast<const R *>(p.s) + base, i) : 0.f;
-      g[k] = in ? IO<T>::get(static_cast<const T *>(p.dy) + base, i) : 0.f;
+      if constexpr (DRO) {
+        o[k] = R(0);
+        if (live && k * tpr + tid < dim) o[k] = static_cast<const R *>(p.dres_out)[base + k * tpr];
+      }
+      c[k] = IO<R>::get(&s[k], 0);
+      g[k] = IO<T>::get(&d[k], 0);
       sum[0] += c[k];
     }
-    row_sums<1>(sum, wpr, threadIdx.x / tpr, red[0]);
-    const float m = sum[0] / n;
+    load(row + step);
+    row_sums<1>(sum, wpr, group, red[0]);
+    const float m = sum[0] * inv;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = k * tpr + tid;
       c[k] -= m;
       if (i < dim) grad_terms(c[k], g[k], __ldg(p.w + i), s3);
     }
-    row_sums<3>(s3, wpr, threadIdx.x / tpr, red[1]);
-    const float r = 1.f / sqrtf(s3[0] / n + p.eps), k1 = s3[1] / n * r, k2 = s3[2] / n;
+    row_sums<3>(s3, wpr, group, red[1]);
+    const float r = rsqrtf(fmaf(s3[0], inv, p.eps)), k1 = s3[1] * inv * r, k2 = s3[2] * inv;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = k * tpr + tid;
@@ -530,18 +561,18 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : NV <= 4 ? 3 : 2) 
       const float q = c[k] * r, wd = __fmul_rn(__ldg(p.w + i), g[k]);
       dw[k] = fmaf(g[k], q, dw[k]);
       db[k] += g[k];
-      float o = p.dres_out ? IO<R>::get(static_cast<const R *>(p.dres_out) + base, i) : 0.f;
-      o = fmaf(r, (wd - k2) - q * k1, o);
-      IO<T>::store1(static_cast<T *>(p.dx) + base, i, o);
-      if (p.dres) IO<R>::store1(static_cast<R *>(p.dres) + base, i, o);
+      float v = DRO ? IO<R>::get(&o[k], 0) : 0.f;
+      v = fmaf(r, fmaf(q, -k1, wd - k2), v);
+      IO<T>::store1(static_cast<T *>(p.dx), base + k * tpr, v);
+      if constexpr (sizeof(R) != sizeof(T)) IO<R>::store1(static_cast<R *>(p.dres), base + k * tpr, v);
     }
   }
   float *part = p.part + (int64_t)blockIdx.x * 2 * p.dim;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = k * tpr + tid;
-    block_part(acc, dw[k], tpr, rpb, part + i, i < dim);
-    block_part(acc, db[k], tpr, rpb, part + p.dim + i, i < dim);
+    block_part(acc, dw[k], tpr, groups, part + i, i < dim);
+    block_part(acc, db[k], tpr, groups, part + p.dim + i, i < dim);
   }
 }
 
@@ -682,26 +713,64 @@ cudaError_t norm_rows(const NormParams &p, const RowShape &sh, int sms, cudaStre
 
 template <typename T, typename R, bool RES>
 cudaError_t norm_vec(const NormParams &p, int sms, cudaStream_t s) {
-  const RowShape sh = row_shape(p.dim, p.rows, sms);
-  // two rows at a time while the next rows' registers (4 a piece in bf16, 8 in fp32) allow
+  RowShape sh = row_shape(p.dim, p.rows, sms);
   constexpr int BYTES = (int)sizeof(T) + (RES ? (int)sizeof(R) : 0);
-  constexpr int RB = BYTES <= 6 ? 2 : 1, MINB = BYTES <= 2 ? 3 : 2;
+  if constexpr (BYTES <= 2) {
+    // bf16 alone is bound by instructions as much as by memory: 32 values a thread, of one
+    // row or of several, in blocks of 4 warps (16384 columns: 16).  Measured at 32768 x 4096:
+    // 105 us; 109 us with 2 rows of 16 values in blocks of 8 warps, 118 us with one.
+    if (p.rows * ((p.dim + 1023) / 1024) >= 8 * (int64_t)sms) {
+      sh.nv = p.dim <= 256 ? 1 : p.dim <= 512 ? 2 : 4;
+      sh.wpr = (int)((p.dim + 256 * sh.nv - 1) / (256 * sh.nv));
+      sh.threads = sh.wpr == 1 || sh.wpr == 2 ? 128 : 32 * sh.wpr;
+      if (sh.nv == 1) return norm_rows<T, R, RES, 1, 4, 1, 128, 4>(p, sh, sms, s);
+      if (sh.nv == 2) return norm_rows<T, R, RES, 2, 2, 1, 128, 4>(p, sh, sms, s);
+      if (sh.threads <= 128) return norm_rows<T, R, RES, 4, 1, 1, 128, 4>(p, sh, sms, s);
+      if (sh.threads <= 256) return norm_rows<T, R, RES, 4, 1, 2, 256, 2>(p, sh, sms, s);
+      return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, sh, sms, s);
+    }
+  }
+  // two rows at a time while the next rows' registers (4 a piece in bf16, 8 in fp32) allow
+  constexpr int RB = BYTES <= 6 ? 2 : 1;
   if (sh.nv == 1) {
-    if (sh.threads <= 256) return norm_rows<T, R, RES, 1, 1, 2, 256, 4>(p, sh, sms, s);
+    if (sh.threads <= 256) return norm_rows<T, R, RES, 1, RB, 2, 256, RB == 2 ? 3 : 4>(p, sh, sms, s);
     return norm_rows<T, R, RES, 1, 1, 4, 512, 2>(p, sh, sms, s);
   }
   if (sh.nv == 2) {
-    if (sh.threads <= 256) return norm_rows<T, R, RES, 2, RB, 2, 256, MINB>(p, sh, sms, s);
+    if (sh.threads <= 256) return norm_rows<T, R, RES, 2, RB, 2, 256, 2>(p, sh, sms, s);
     return norm_rows<T, R, RES, 2, 1, 4, 512, 1>(p, sh, sms, s);
   }
   return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, sh, sms, s);
 }
 
-template <typename T, typename R, int NV>
-cudaError_t norm_nv(const NormParams &p, int wpr, cudaStream_t s) {
-  const int threads = std::max(128, 32 * wpr), rpb = threads / (32 * wpr);
-  k_norm<T, R, NV><<<(unsigned)((p.rows + rpb - 1) / rpb), threads, 0, s>>>(p, wpr);
+// Columns one by one: 8 a thread up to 4096 columns, 16 and 32 beyond.
+RowShape elem_shape(int64_t dim, int64_t rows, int sms) {
+  RowShape r;
+  r.nv = dim <= 4096 ? 8 : dim <= 8192 ? 16 : 32;
+  r.wpr = (int)((dim + 32 * r.nv - 1) / (32 * r.nv));
+  if (r.wpr <= 4) {  // several rows a block: a power of two of warps each
+    while (r.wpr & (r.wpr - 1)) ++r.wpr;
+    r.threads = 256;
+  } else {
+    r.threads = 32 * r.wpr;
+  }
+  return r;
+}
+
+template <typename T, typename R, bool RES, int NV, int MAXT, int MINB>
+cudaError_t norm_elems(const NormParams &p, const RowShape &sh, int sms, cudaStream_t s) {
+  const int rows = sh.threads / (32 * sh.wpr);
+  const int64_t need = (p.rows + rows - 1) / rows, fit = (int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads);
+  k_norm_elems<T, R, RES, NV, MAXT, MINB><<<(unsigned)std::min(need, fit), sh.threads, 0, s>>>(p, sh.wpr);
   return cudaGetLastError();
+}
+
+template <typename T, typename R, bool RES>
+cudaError_t norm_scalar(const NormParams &p, int sms, cudaStream_t s) {
+  const RowShape sh = elem_shape(p.dim, p.rows, sms);
+  if (sh.nv == 8)
+    return sh.threads <= 256 ? norm_elems<T, R, RES, 8, 256, 5>(p, sh, sms, s) : norm_elems<T, R, RES, 8, 512, 2>(p, sh, sms, s);
+  return sh.nv == 16 ? norm_elems<T, R, RES, 16, 512, 1>(p, sh, sms, s) : norm_elems<T, R, RES, 32, 512, 1>(p, sh, sms, s);
 }
 
 template <typename T, typename R>
@@ -715,16 +784,7 @@ cudaError_t norm_t(const NormParams &p, int sms, cudaStream_t s) {
     return cudaGetLastError();
   }
   if (vec) return p.res ? norm_vec<T, R, true>(p, sms, s) : norm_vec<T, R, false>(p, sms, s);
-  // the fewest warps a row that hold it at 32 values a thread; more while the rows leave
-  // the machine empty
-  int wpr = 1;
-  while (wpr * 32 * 32 < p.dim) wpr *= 2;
-  while (wpr < 16 && p.rows * wpr < 16 * sms && wpr * 32 < p.dim) wpr *= 2;
-  const int nv = (int)((p.dim + 32 * wpr - 1) / (32 * wpr));
-  if (nv <= 4) return norm_nv<T, R, 4>(p, wpr, s);
-  if (nv <= 8) return norm_nv<T, R, 8>(p, wpr, s);
-  if (nv <= 16) return norm_nv<T, R, 16>(p, wpr, s);
-  return norm_nv<T, R, 32>(p, wpr, s);
+  return p.res ? norm_scalar<T, R, true>(p, sms, s) : norm_scalar<T, R, false>(p, sms, s);
 }
 
 // blocks of the backward: enough to fill the machine, no more than there are rows
@@ -747,9 +807,22 @@ cudaError_t bwd_rows(const NormBwdParams &p, const RowShape &sh, int sms, cudaSt
 
 template <typename T, typename R, bool DRO>
 cudaError_t bwd_vec(const NormBwdParams &p, int sms, cudaStream_t s) {
-  const RowShape sh = row_shape(p.dim, p.rows, sms);
+  RowShape sh = row_shape(p.dim, p.rows, sms);
+  if constexpr (DRO) {
+    // a third tensor in registers ahead: 8 values a thread up to 4096 columns
+    if (p.dim <= 4096) {
+      sh.nv = 1;
+      sh.wpr = (int)((p.dim + 255) / 256);
+      if (sh.wpr <= 4) {
+        while (sh.wpr & (sh.wpr - 1)) ++sh.wpr;
+        sh.threads = 256;
+      } else {
+        sh.threads = 32 * sh.wpr;
+      }
+    }
+  }
   if (sh.nv == 1) {
-    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, 3>(p, sh, sms, s);
+    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, sizeof(R) == 2 ? 3 : 2>(p, sh, sms, s);
     return bwd_rows<T, R, DRO, 1, 4, 512, 1>(p, sh, sms, s);
   }
   if (sh.nv == 2) {
@@ -759,14 +832,22 @@ cudaError_t bwd_vec(const NormBwdParams &p, int sms, cudaStream_t s) {
   return bwd_rows<T, R, DRO, 4, 4, 512, 1>(p, sh, sms, s);
 }
 
-template <typename T, typename R, int NV, int THREADS>
-cudaError_t bwd_plain(const NormBwdParams &p, int wpr, int sms, cudaStream_t s) {
-  const int rpb = THREADS / (32 * wpr);
-  const int64_t fit = (int64_t)sms * (THREADS > 256 ? 1 : NV <= 4 ? 3 : 2);
-  const int64_t blocks = std::min(std::min((p.rows + rpb - 1) / rpb, fit), bwd_blocks_for(p.rows, sms));
-  k_norm_bwd<T, R, NV, THREADS><<<(unsigned)blocks, THREADS, 0, s>>>(p, wpr);
+template <typename T, typename R, bool DRO, int NV, int MAXT, int MINB>
+cudaError_t bwd_elems(const NormBwdParams &p, const RowShape &sh, int sms, cudaStream_t s) {
+  const int groups = sh.threads / (32 * sh.wpr);
+  const int64_t fit = (int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads);
+  const int64_t blocks = std::min(std::min((p.rows + groups - 1) / groups, fit), bwd_blocks_for(p.rows, sms));
+  k_norm_bwd_elems<T, R, DRO, NV, MAXT, MINB><<<(unsigned)blocks, sh.threads, 0, s>>>(p, sh.wpr);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : norm_parts(p, blocks, s);
+}
+
+template <typename T, typename R, bool DRO>
+cudaError_t bwd_scalar(const NormBwdParams &p, int sms, cudaStream_t s) {
+  const RowShape sh = elem_shape(p.dim, p.rows, sms);
+  if (sh.nv == 8)
+    return sh.threads <= 256 ? bwd_elems<T, R, DRO, 8, 256, 3>(p, sh, sms, s) : bwd_elems<T, R, DRO, 8, 512, 1>(p, sh, sms, s);
+  return bwd_elems<T, R, DRO, 16, 512, 1>(p, sh, sms, s);
 }
 
 template <typename T, typename R>
@@ -786,12 +867,7 @@ cudaError_t norm_bwd_t(const NormBwdParams &p, int sms, cudaStream_t s) {
     e = cudaGetLastError();
     return e != cudaSuccess ? e : norm_parts(p, splits, s);
   }
-  int wpr = 1;
-  while (wpr < 8 && wpr * 128 < p.dim) wpr *= 2;
-  if (p.dim <= 1024) return bwd_plain<T, R, 4, 256>(p, wpr, sms, s);
-  if (p.dim <= 2048) return bwd_plain<T, R, 8, 256>(p, 8, sms, s);
-  if (p.dim <= 4096) return bwd_plain<T, R, 16, 256>(p, 8, sms, s);
-  return bwd_plain<T, R, 16, 512>(p, 16, sms, s);
+  return p.dres_out ? bwd_scalar<T, R, true>(p, sms, s) : bwd_scalar<T, R, false>(p, sms, s);
 }
 
 }  // namespace
