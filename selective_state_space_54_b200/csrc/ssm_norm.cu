@@ -679,7 +679,7 @@ bool a32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kWidest = 16384;     // columns that 16 warps hold at 32 values a thread
-constexpr int kWidestPlain = 8192; // the same without 16-byte accesses, backward
+constexpr int kWidestBwd = 8192;   // backward, 16 values a thread beside their sums
 
 // Warps a row and pieces of 8 values a thread: up to 2048 columns 1, 2 or 4 warps (blocks
 // of 8 warps hold several rows), above that a block a row, as many warps as 16 values a
@@ -808,28 +808,28 @@ cudaError_t bwd_rows(const NormBwdParams &p, const RowShape &sh, int sms, cudaSt
 template <typename T, typename R, bool DRO>
 cudaError_t bwd_vec(const NormBwdParams &p, int sms, cudaStream_t s) {
   RowShape sh = row_shape(p.dim, p.rows, sms);
-  if constexpr (DRO) {
-    // a third tensor in registers ahead: 8 values a thread up to 4096 columns
-    if (p.dim <= 4096) {
-      sh.nv = 1;
-      sh.wpr = (int)((p.dim + 255) / 256);
-      if (sh.wpr <= 4) {
-        while (sh.wpr & (sh.wpr - 1)) ++sh.wpr;
-        sh.threads = 256;
-      } else {
-        sh.threads = 32 * sh.wpr;
-      }
+  // with the residual's gradient on an fp32 stream a third tensor waits in registers: 8
+  // values a thread up to 4096 columns (16384 x 4096: 192 us, 261 us with 16)
+  constexpr bool WIDE = DRO && sizeof(R) == 4;
+  if (WIDE && p.dim <= 4096) {
+    sh.nv = 1;
+    sh.wpr = (int)((p.dim + 255) / 256);
+    if (sh.wpr <= 4) {
+      while (sh.wpr & (sh.wpr - 1)) ++sh.wpr;
+      sh.threads = 256;
+    } else {
+      sh.threads = 32 * sh.wpr;
     }
   }
   if (sh.nv == 1) {
-    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, sizeof(R) == 2 ? 3 : 2>(p, sh, sms, s);
+    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, WIDE ? 2 : 3>(p, sh, sms, s);
     return bwd_rows<T, R, DRO, 1, 4, 512, 1>(p, sh, sms, s);
   }
-  if (sh.nv == 2) {
-    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 2, 2, 256, 2>(p, sh, sms, s);
-    return bwd_rows<T, R, DRO, 2, 4, 512, 1>(p, sh, sms, s);
+  if (sh.threads <= 256) return bwd_rows<T, R, DRO, 2, 2, 256, WIDE ? 1 : 2>(p, sh, sms, s);
+  if constexpr (WIDE) {  // 204 registers a thread: none spills
+    if (sh.threads <= 320) return bwd_rows<T, R, DRO, 2, 4, 320, 1>(p, sh, sms, s);
   }
-  return bwd_rows<T, R, DRO, 4, 4, 512, 1>(p, sh, sms, s);
+  return bwd_rows<T, R, DRO, 2, 4, 512, 1>(p, sh, sms, s);
 }
 
 template <typename T, typename R, bool DRO, int NV, int MAXT, int MINB>
@@ -846,7 +846,7 @@ template <typename T, typename R, bool DRO>
 cudaError_t bwd_scalar(const NormBwdParams &p, int sms, cudaStream_t s) {
   const RowShape sh = elem_shape(p.dim, p.rows, sms);
   if (sh.nv == 8)
-    return sh.threads <= 256 ? bwd_elems<T, R, DRO, 8, 256, 3>(p, sh, sms, s) : bwd_elems<T, R, DRO, 8, 512, 1>(p, sh, sms, s);
+    return sh.threads <= 256 ? bwd_elems<T, R, DRO, 8, 256, 2>(p, sh, sms, s) : bwd_elems<T, R, DRO, 8, 512, 1>(p, sh, sms, s);
   return bwd_elems<T, R, DRO, 16, 512, 1>(p, sh, sms, s);
 }
 
@@ -855,8 +855,8 @@ cudaError_t norm_bwd_t(const NormBwdParams &p, int sms, cudaStream_t s) {
   auto at = [](const void *q, size_t es) { return es == 4 ? a32(q) : a16(q); };  // 8 values
   const bool vec = p.dim % 8 == 0 && at(p.s, sizeof(R)) && at(p.dy, sizeof(T)) && at(p.dres_out, sizeof(R)) &&
                    at(p.dx, sizeof(T)) && at(p.dres, sizeof(R)) && a16(p.w);
-  if (vec && p.dim <= kWidest) return p.dres_out ? bwd_vec<T, R, true>(p, sms, s) : bwd_vec<T, R, false>(p, sms, s);
-  if (p.dim > kWidestPlain) {
+  if (vec && p.dim <= kWidestBwd) return p.dres_out ? bwd_vec<T, R, true>(p, sms, s) : bwd_vec<T, R, false>(p, sms, s);
+  if (p.dim > kWidestBwd) {
     const int64_t splits = bwd_blocks_for((p.rows + 31) / 32, sms);
     float2 *stats = reinterpret_cast<float2 *>(p.part + splits * 2 * p.dim);
     if (vec) k_norm_bwd_wide<T, R, 8><<<(unsigned)p.rows, kWideThreads, 0, s>>>(p, stats);
@@ -878,7 +878,7 @@ cudaError_t launch_norm(int io_dtype, int res_dtype, const NormParams &p, int sm
 }
 
 size_t norm_bwd_part_floats(int64_t rows, int64_t dim, int sms) {
-  return (size_t)bwd_blocks_for(rows, sms) * 2 * (size_t)dim + (dim > kWidestPlain ? 2 * (size_t)rows : 0);
+  return (size_t)bwd_blocks_for(rows, sms) * 2 * (size_t)dim + (dim > kWidestBwd ? 2 * (size_t)rows : 0);
 }
 
 cudaError_t launch_norm_bwd(int io_dtype, int res_dtype, const NormBwdParams &p, int sms, cudaStream_t s) {
