@@ -391,14 +391,32 @@ def _gated_step_ref(batch, dim, io_dtype, flags):
     return ctypes.byref(_gated_shape(batch, dim, 1, io_dtype, SSM_PATH_AUTO, flags))
 
 
-def gated_scan_shape(u, *, tied=True, save_states=False, token_major=False, path: int = SSM_PATH_AUTO) -> ssm_shape:
-    """The shape of a gated_scan_fwd / gated_scan_bwd call on ``u``, for the workspace queries."""
+def _gated_key(u, tied, save_states, token_major, path):
     if u.dim() != 3:
         raise ValueError(f"u has shape {tuple(u.shape)}, expected three axes")
-    batch, seqlen, dim = u.shape if token_major else (u.shape[0], u.shape[2], u.shape[1])
-    flags = ((0 if tied else SSM_FLAG_UNTIED) | (SSM_FLAG_SAVE_STATES if save_states else 0)
-             | (SSM_FLAG_TOKEN_MAJOR if token_major else 0))
-    return _gated_shape(batch, dim, seqlen, _io_dtype(u), path, flags)
+    batch, dim, seqlen = u.shape
+    flags = 0 if tied else SSM_FLAG_UNTIED
+    if save_states:
+        flags |= SSM_FLAG_SAVE_STATES
+    if token_major:
+        flags |= SSM_FLAG_TOKEN_MAJOR
+        dim, seqlen = seqlen, dim
+    return batch, dim, seqlen, _io_dtype(u), path, flags
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_plan(key, device_index):
+    """(shape, reference to it, forward and backward workspace bytes on the device)."""
+    import torch
+    shape = _gated_shape(*key)
+    with torch.cuda.device(device_index):
+        return (shape, ctypes.byref(shape), gated_scan_fwd_workspace_bytes(shape),
+                gated_scan_bwd_workspace_bytes(shape))
+
+
+def gated_scan_shape(u, *, tied=True, save_states=False, token_major=False, path: int = SSM_PATH_AUTO) -> ssm_shape:
+    """The shape of a gated_scan_fwd / gated_scan_bwd call on ``u``, for the workspace queries."""
+    return _gated_shape(*_gated_key(u, tied, save_states, token_major, path))
 
 
 def gated_scan_fwd_workspace_bytes(shape: ssm_shape) -> int:
@@ -453,7 +471,7 @@ def gated_scan_fwd(u, f, z=None, f_bias=None, *, tied=True, starts=None, initial
     on the tensors' device, on ``stream`` or that device's current one."""
     import torch
     dev = _cuda_device("u", u)
-    shape = gated_scan_shape(u, tied=tied, save_states=save_states, token_major=token_major, path=path)
+    shape, ref, nbytes, _ = _gated_plan(_gated_key(u, tied, save_states, token_major, path), dev.index)
     _check_gated(shape, u, f, z, f_bias, starts, initial_state)
     if save_states and workspace is None:
         raise ValueError("save_states writes into the workspace: pass workspace=")
@@ -463,15 +481,13 @@ def gated_scan_fwd(u, f, z=None, f_bias=None, *, tied=True, starts=None, initial
     if last_state is not None:
         _check_io("last_state", last_state, states, torch.float32, dev)
     lib = _lib.load()
-    ref = ctypes.byref(shape)
 
     def call(handle):
         out = torch.empty_like(u) if y is None else y
         last = last_state
         if last is None and return_last_state:
-            last = torch.empty(states, dtype=torch.float32, device=dev)
-        nbytes = lib.ssm_gated_scan_fwd_workspace_bytes(ref)
-        ws = _workspace_for(nbytes, dev, workspace)
+            last = u.new_empty(states, dtype=torch.float32)
+        ws = None if workspace is None and nbytes == 0 else _workspace_for(nbytes, dev, workspace)
         rc = lib.ssm_gated_scan_fwd(ref, u.data_ptr(), f.data_ptr(), _addr(z), _addr(f_bias), _addr(starts),
                                     _addr(initial_state), out.data_ptr(), _addr(last), _addr(ws),
                                     0 if ws is None else ws.nbytes, handle)
@@ -493,28 +509,28 @@ def gated_scan_bwd(u, f, z, f_bias, dout, *, tied=True, starts=None, initial_sta
     of a gated_scan_fwd(save_states=True) call on the same inputs, with the same ``path``."""
     import torch
     dev = _cuda_device("u", u)
-    shape = gated_scan_shape(u, tied=tied, save_states=fwd_workspace is not None, token_major=token_major, path=path)
+    shape, ref, fwd_bytes, nbytes = _gated_plan(
+        _gated_key(u, tied, fwd_workspace is not None, token_major, path), dev.index)
     _check_gated(shape, u, f, z, f_bias, starts, initial_state)
     f32, states, per = torch.float32, (shape.batch, shape.dim), (shape.dim,)
     _check_io("dout", dout, u.shape, u.dtype, dev)
     _check_io("dlast_state", dlast_state, states, f32, dev)
     lib = _lib.load()
-    ref = ctypes.byref(shape)
     given = out or {}
+    if fwd_workspace is not None:
+        _workspace_for(fwd_bytes, dev, fwd_workspace)
 
     def gradient(name, like, shp, ty):
         if given.get(name) is not None:
             _check_io(name, given[name], shp, ty, dev)
             return given[name]
-        return None if like is None else torch.empty(shp, dtype=ty, device=dev)
+        return None if like is None else u.new_empty(shp, dtype=ty)
 
     def call(handle):
-        if fwd_workspace is not None:
-            _workspace_for(lib.ssm_gated_scan_fwd_workspace_bytes(ref), dev, fwd_workspace)
         g = {"du": gradient("du", u, u.shape, u.dtype), "df": gradient("df", u, u.shape, u.dtype),
              "dz": gradient("dz", z, u.shape, u.dtype), "df_bias": gradient("df_bias", f_bias, per, f32),
              "dinitial_state": gradient("dinitial_state", u if want_dinitial_state else None, states, f32)}
-        ws = _workspace_for(lib.ssm_gated_scan_bwd_workspace_bytes(ref), dev, workspace)
+        ws = _workspace_for(nbytes, dev, workspace)
         rc = lib.ssm_gated_scan_bwd(
             ref, u.data_ptr(), f.data_ptr(), _addr(z), _addr(f_bias), _addr(starts), _addr(initial_state),
             dout.data_ptr(), _addr(dlast_state), _addr(fwd_workspace), g["du"].data_ptr(), g["df"].data_ptr(),

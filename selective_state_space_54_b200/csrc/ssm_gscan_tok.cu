@@ -53,18 +53,40 @@ __device__ __noinline__ void fill_slot_narrow(unsigned char *slot, const T *src,
   constexpr int RUN = Tok<T>::RUN, ROW = Tok<T>::ROW;
   if (mode == 1) {
     constexpr int E = 4 / (int)sizeof(T), PER = ROW / 128;  // rounds a token
-    const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
-#pragma unroll 4
-    for (int j = 0; j < RUN * PER; ++j) {
-      const int t = j / PER, c = (j % PER * 32 + lane) * E;
-      const bool in = c < ch && t < n;
-      copy4(s + 4 * (j * 32 + lane), in ? src + t * dim + c : src, in);
+    uint32_t s = (uint32_t)__cvta_generic_to_shared(slot) + 4 * lane;
+    const T *q = src + lane * E;
+    if (n == RUN && ch == kTokChannels) {
+#pragma unroll
+      for (int t = 0; t < RUN; ++t) {
+#pragma unroll
+        for (int h = 0; h < PER; ++h) copy4(s + 128 * (t * PER + h), q + 32 * E * h, true);
+        q += dim;
+      }
+    } else {
+#pragma unroll 2
+      for (int t = 0; t < RUN; ++t) {
+#pragma unroll
+        for (int h = 0; h < PER; ++h) {
+          const bool in = t < n && (h * 32 + lane) * E < ch;
+          copy4(s + 128 * (t * PER + h), in ? q + 32 * E * h : src, in);
+        }
+        q += dim;
+      }
     }
   } else {
-#pragma unroll 8
-    for (int j = 0; j < 2 * RUN; ++j) {
-      const int t = j / 2, c = j % 2 * 32 + lane;
-      *reinterpret_cast<T *>(slot + t * ROW + c * (int)sizeof(T)) = c < ch && t < n ? src[t * dim + c] : T(0);
+    const T *q = src + lane;
+    T v[RUN][2];
+#pragma unroll
+    for (int t = 0; t < RUN; ++t) {
+      v[t][0] = t < n && lane < ch ? q[0] : T(0);
+      v[t][1] = t < n && lane + 32 < ch ? q[32] : T(0);
+      q += dim;
+    }
+#pragma unroll
+    for (int t = 0; t < RUN; ++t) {
+      T *d = reinterpret_cast<T *>(slot + t * ROW) + lane;
+      d[0] = v[t][0];
+      d[32] = v[t][1];
     }
   }
 }
@@ -75,12 +97,20 @@ __device__ __forceinline__ void fill_slot(unsigned char *slot, const T *src, int
   const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot) + 16 * lane;
   const int t = lane / PER, c = lane % PER * E;
   const T *q = src + t * dim + c;
-  const int left = c < ch ? n - t : 0;
+  if (n == Tok<T>::RUN && ch == kTokChannels) {
 #pragma unroll
-  for (int j = 0; j < Tok<T>::RUN / STEP; ++j) {
-    const bool in = j * STEP < left;
-    copy16(s + 512 * j, in ? q : src, in);
-    q += STEP * dim;
+    for (int j = 0; j < Tok<T>::RUN / STEP; ++j) {
+      copy16(s + 512 * j, q, true);
+      q += STEP * dim;
+    }
+  } else {
+    const int left = c < ch ? n - t : 0;
+#pragma unroll 1
+    for (int j = 0; j < Tok<T>::RUN / STEP; ++j) {
+      const bool in = j * STEP < left;
+      copy16(s + 512 * j, in ? q : src, in);
+      q += STEP * dim;
+    }
   }
 }
 
