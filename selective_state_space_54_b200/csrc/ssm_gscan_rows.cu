@@ -355,8 +355,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 5 : 6) k_rows_fw
 // ---- look-back over tiles of a row ---------------------------------------------------
 // Called by one warp of tile `c` of a row (time index; from behind in the backward)
 // with the runs of the tile's warps: publishes the tile's run, and returns the state
-// entering it (with one tile a group the caller, which walks the warps' runs anyway,
-// publishes the state leaving it instead).  The tiles of a group of p.group are joined in the order of their index whatever
+// entering it.  The tiles of a group of p.group are joined in the order of their index whatever
 // the order they finish in, starting from the state that the last tile of the group before
 // published; so the result does not depend on timing.  `w` holds what the lane saw of the
 // word it needs when it looked ahead (peek): lane i the run of the group's tile i, lane 31
@@ -380,11 +379,9 @@ __device__ __forceinline__ float look_back(const GsParams &p, int64_t row, unsig
   const unsigned g = c / p.group, in = c - g * p.group;
   const bool last_in_group = in == p.group - 1;
   Run tile = no_run();
-  if (p.group > 1) {
 #pragma unroll
-    for (int i = 0; i < kGsTileWarps; ++i) tile = join<ST>(runs[FROM_BEHIND ? kGsTileWarps - 1 - i : i], tile);
-    if (lane == 0 && !last_in_group) put_run(p.runs + row * p.tiles + c, tile);
-  }
+  for (int i = 0; i < kGsTileWarps; ++i) tile = join<ST>(runs[FROM_BEHIND ? kGsTileWarps - 1 - i : i], tile);
+  if (lane == 0 && !last_in_group) put_run(p.runs + row * p.tiles + c, tile);
   unsigned long long started = 0;
   unsigned n = 0;
   auto wait = [&]() {
@@ -411,18 +408,79 @@ __device__ __forceinline__ float look_back(const GsParams &p, int64_t row, unsig
     h = __shfl_sync(kAll, of_word((unsigned)w), 31);
   }
   if (in > 0) h = run_on<ST>(r, h);
-  if (lane == 0 && last_in_group && p.group > 1) put_state(p.states + row * p.groups + g, run_on<ST>(tile, h));
+  if (lane == 0 && last_in_group) put_state(p.states + row * p.groups + g, run_on<ST>(tile, h));
   return h;
 }
 
 constexpr int kTileThreads = 32 * kGsTileWarps;
 
-// A tile of a row: where, and its chunk of this warp
 struct TileShared {
   Taken ticket;
-  Run run[kGsTileWarps];
+  Run run[2][kGsTileWarps];  // of this tile and the one before: one barrier a tile is enough
   float in[kGsTileWarps], db[kGsTileWarps];
 };
+
+// The value entering the warp's own run, after the barrier that shows the warps' runs;
+// FROM_BEHIND: the walk starts at the last warp.  `first` enters the row's first tile; the
+// value leaving the tile is published, and goes to `end` where it leaves the row.  With one
+// tile a group every warp reads the state itself and walks the runs before its own; else
+// warp 0 looks back for all.  q, seen: as in look_back (one tile a group: in every warp, the
+// state of the tile before, in every lane).
+template <bool ST, bool FROM_BEHIND>
+__device__ __forceinline__ float tile_in(const GsParams &p, TileShared &sm, const Run *runs, int64_t row, unsigned c,
+                                         float first, const void *q, unsigned long long seen, float *end) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int mine = FROM_BEHIND ? kGsTileWarps - 1 - w : w;
+  auto nth = [](int i) { return FROM_BEHIND ? kGsTileWarps - 1 - i : i; };
+  if (p.group == 1) {
+    float h = first;
+    if (q) {
+      unsigned long long started = 0;
+      unsigned n = 0, v = (unsigned)seen;
+      while (v == 0u) {
+        v = look32(static_cast<const unsigned *>(q));
+        if (v == 0u && !spun(started, n, p.err)) break;
+      }
+      h = of_word(v);
+    }
+#pragma unroll
+    for (int i = 0; i < kGsTileWarps - 1; ++i) {
+      if (i < mine) h = run_on<ST>(runs[nth(i)], h);
+    }
+    if (mine == kGsTileWarps - 1 && lane == 0) {
+      const float out = run_on<ST>(runs[w], h);
+      if (c + 1 < p.tiles) put_state(p.states + row * p.groups + c, out);
+      else if (end) end[row] = out;
+    }
+    return h;
+  }
+  if (w == 0) {
+    float h = look_back<ST, FROM_BEHIND>(p, row, c, first, runs, q, seen);
+#pragma unroll
+    for (int i = 0; i < kGsTileWarps; ++i) {
+      if (lane == 0) sm.in[nth(i)] = h;
+      h = run_on<ST>(runs[nth(i)], h);
+    }
+    if (lane == 0 && c + 1 == p.tiles && end) end[row] = h;
+  }
+  __syncthreads();
+  return sm.in[w];
+}
+// where a tile's state comes from, and what is seen there ahead
+__device__ __forceinline__ const void *tile_look(const GsParams &p, int64_t row, unsigned c, unsigned long long &seen) {
+  const void *q = nullptr;
+  seen = 0ull;
+  if (p.group == 1) {
+    if (c > 0) {
+      q = p.states + row * p.groups + c - 1;
+      seen = look32(static_cast<const unsigned *>(q));
+    }
+  } else if (threadIdx.x < 32) {
+    q = look_at(p, row, c);
+    seen = peek(q);
+  }
+  return q;
+}
 
 // Blocks stay and take tile after tile: the next tile's ticket is drawn and its steps are on
 // their way while the current one waits for the state entering it.
@@ -447,13 +505,10 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     unsigned char *stage = ring + stg * kStage<Z, false>;
     unsigned drawn = 0;
     if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
-    const void *q = nullptr;
-    unsigned long long seen = 0;
-    if (w == 0) {
-      q = look_at(p, row, at.time);
-      seen = peek(q);
-    }
+    unsigned long long seen;
+    const void *q = tile_look(p, row, at.time, seen);
     const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
+    const float first = at.time < p.group && p.h0 ? p.h0[row] : 0.f;
     unsigned st = 0;
     if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
     copies_wait<0>();
@@ -464,7 +519,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     Run r = join<ST>(hv.hi, hv.lo);
     scan_up<ST>(r, lane, 32);
     const Run before = run_above(r, 32);
-    if (lane == 31) sm.run[w] = r;
+    if (lane == 31) sm.run[stg][w] = r;
     if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, (unsigned)p.dim);
     __syncthreads();
     const Taken next = sm.ticket;
@@ -472,18 +527,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
       fill_stage<T, Z, false>(ring + (stg ^ 1) * kStage<Z, false>, p, next.place.chain,
                               ((int64_t)next.place.time * kGsTileWarps + w) * G::PASS, lanes);
     copies_commit();
-    if (w == 0) {
-      float h = look_back<ST, false>(p, row, at.time, p.h0 ? p.h0[row] : 0.f, sm.run, q, seen);
-#pragma unroll
-      for (int i = 0; i < kGsTileWarps; ++i) {
-        if (lane == 0) sm.in[i] = h;
-        h = run_on<ST>(sm.run[i], h);
-      }
-      if (lane == 0 && p.group == 1) put_state(p.states + row * p.groups + at.time, h);
-      if (lane == 0 && at.time == p.tiles - 1 && p.last) p.last[row] = h;
-    }
-    __syncthreads();
-    const float hw = sm.in[w];
+    const float hw = tile_in<ST, false>(p, sm, sm.run[stg], row, at.time, first, q, seen, p.last);
     if (p.ckpt && lane == 0 && chunk > 0 && chunk < chunks) p.ckpt[row * chunks + chunk] = hw;
     lane_out<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo, t < p.L);
     __syncwarp();
@@ -665,13 +709,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     unsigned char *stage = ring + stg * kStage<Z, true>;
     unsigned drawn = 0;
     if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
-    const void *q = nullptr;
-    unsigned long long seen = 0;
-    if (w == 0) {
-      q = look_at(p, row, at.time);
-      seen = peek(q);
-    }
+    unsigned long long seen;
+    const void *q = tile_look(p, row, at.time, seen);
     const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
+    const float first = at.time < p.group && p.dlast ? p.dlast[row] : 0.f;
     const float h0 = chunk >= chunks ? 0.f : chunk > 0 ? p.ckpt[row * chunks + chunk] : (p.h0 ? p.h0[row] : 0.f);
     unsigned st = 0;
     if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
@@ -686,7 +727,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     scan_down<ST>(g, lane, 32);
     const Run before = run_above(r, 32), after = run_below(g, 32);
     const float hin = lane == 0 ? h0 : run_on<ST>(before, h0);
-    if (lane == 0) sm.run[w] = g;
+    if (lane == 0) sm.run[stg][w] = g;
     if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, (unsigned)p.dim);
     __syncthreads();
     const Taken next = sm.ticket;
@@ -694,18 +735,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
       fill_stage<T, Z, true>(ring + (stg ^ 1) * kStage<Z, true>, p, next.place.chain, chunk_of(next.place.time) * G::PASS,
                              lanes);
     copies_commit();
-    if (w == 0) {
-      float P = look_back<ST, true>(p, row, at.time, p.dlast ? p.dlast[row] : 0.f, sm.run, q, seen);
-#pragma unroll
-      for (int i = kGsTileWarps - 1; i >= 0; --i) {
-        if (lane == 0) sm.in[i] = P;
-        P = run_on<ST>(sm.run[i], P);
-      }
-      if (lane == 0 && p.group == 1) put_state(p.states + row * p.groups + at.time, P);
-      if (lane == 0 && at.time == p.tiles - 1 && p.dh0) p.dh0[row] = P;
-    }
-    __syncthreads();
-    const float pw = sm.in[w];
+    const float pw = tile_in<ST, true>(p, sm, sm.run[stg], row, at.time, first, q, seen, p.dh0);
     float db = lane_grads<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, dh, b2, hin,
                                           lane == 31 ? pw : run_on<ST>(after, pw), hv.lo, gv.hi, t < p.L);
     if (p.dbias_part) {

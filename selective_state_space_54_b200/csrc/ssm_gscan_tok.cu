@@ -192,12 +192,22 @@ __device__ __forceinline__ void cut_at_start(Run2 &r, unsigned st) {
   }
 }
 
+// The warps' runs of this tile and the one before (so one barrier a tile is enough).  The
+// other tile's place also takes the joined runs of a group's earlier tiles, with a barrier
+// more at the tile's end.
 struct TokShared {
   Taken ticket;
-  f2 A[kTokWarps][32], N[kTokWarps][32], B[kTokWarps][32];  // the warps' runs
-  f2 other[kTokWarps][32];                                  // backward: B of the state's runs; sums
-  f2 gA[kTokWarps][32], gN[kTokWarps][32], gB[kTokWarps][32];  // those of the group's earlier tiles
-  __device__ __forceinline__ Run2 of(int w, int lane) const { return {A[w][lane], N[w][lane], B[w][lane]}; }
+  f2 A[2][kTokWarps][32], N[2][kTokWarps][32], B[2][kTokWarps][32];
+  __device__ __forceinline__ Run2 of(int k, int w, int lane) const { return {A[k][w][lane], N[k][w][lane], B[k][w][lane]}; }
+  __device__ __forceinline__ void put(int k, int w, int lane, const Run2 &r) {
+    A[k][w][lane] = r.A;
+    N[k][w][lane] = r.N;
+    B[k][w][lane] = r.B;
+  }
+};
+struct TokSharedBwd : TokShared {
+  f2 state[2][kTokWarps][32];  // B of the state's runs
+  f2 sum[kTokWarps][32];
 };
 
 // a pair of states as one word of 64 bits
@@ -233,7 +243,7 @@ __device__ __forceinline__ const unsigned long long *state_of(const GsParams &p,
 // earlier tiles are joined in the order of their index, a quarter by each warp, before the
 // state is waited for: from there to the state leaving the tile it is a few steps.
 template <bool ST, bool FROM_BEHIND>
-__device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t chain, unsigned c, f2 first, int w,
+__device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int cur, int64_t chain, unsigned c, f2 first, int w,
                                       int lane, const unsigned long long *q, unsigned long long seen, f2 &out) {
   const unsigned g = c / p.group, in = c - g * p.group;
   const bool last = c == p.tiles - 1, last_in_group = in == p.group - 1;
@@ -242,9 +252,9 @@ __device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t 
   if (p.group > 1) {
     unsigned long long *runs = p.runs + chain * p.tiles * kTokChannels;
     if (mine == 0 && !last && !last_in_group) {
-      Run2 tile = sm.of(nth(0), lane);
+      Run2 tile = sm.of(cur, nth(0), lane);
 #pragma unroll
-      for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(nth(j), lane), tile);
+      for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(cur, nth(j), lane), tile);
       Run x, y;
       split(tile, x, y);
       put_run(runs + (int64_t)c * kTokChannels + 2 * lane, x);
@@ -271,9 +281,7 @@ __device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t 
           y = join<ST>(of_words(wait64(a + j * kTokChannels + 1, v[j][1], p.err)), y);
         }
       }
-      sm.gA[mine][lane] = pack2(x.A, y.A);
-      sm.gN[mine][lane] = pack2(x.N, y.N);
-      sm.gB[mine][lane] = pack2(x.B, y.B);
+      sm.put(cur ^ 1, mine, lane, {pack2(x.A, y.A), pack2(x.N, y.N), pack2(x.B, y.B)});
       __syncthreads();
     }
   }
@@ -281,14 +289,14 @@ __device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int64_t 
   if (q) h = of_pair(wait64(q, seen, p.err));
   if (in > 0) {
 #pragma unroll
-    for (int j = 0; j < kTokWarps; ++j) h = run_on2<ST>({sm.gA[j][lane], sm.gN[j][lane], sm.gB[j][lane]}, h);
+    for (int j = 0; j < kTokWarps; ++j) h = run_on2<ST>(sm.of(cur ^ 1, j, lane), h);
   }
 #pragma unroll
   for (int j = 0; j < kTokWarps - 1; ++j) {
-    if (j < mine) h = run_on2<ST>(sm.of(nth(j), lane), h);
+    if (j < mine) h = run_on2<ST>(sm.of(cur, nth(j), lane), h);
   }
   if (mine == kTokWarps - 1) {
-    out = run_on2<ST>(sm.of(w, lane), h);
+    out = run_on2<ST>(sm.of(cur, w, lane), h);
     if (!last && last_in_group)
       put_pair_state(reinterpret_cast<unsigned long long *>(p.states) + (chain * p.groups + g) * 32 + lane, out);
   }
@@ -375,16 +383,14 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     __syncwarp();
     f2 ng[RUN];
     const Run2 r = warp_run<T, TIED, ST>(ng, stage, a.n, b2, st, lane);
-    sm.A[w][lane] = r.A;
-    sm.N[w][lane] = r.N;
-    sm.B[w][lane] = r.B;
+    sm.put(stg, w, lane, r);
     if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
     __syncthreads();
     const Taken next = sm.ticket;
     if (next.id < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next.place, w), lane);
     copies_commit();
     f2 out;
-    f2 h = tile_in<ST, false>(p, sm, at.chain, at.time, first, w, lane, q, seen, out);
+    f2 h = tile_in<ST, false>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
     if (p.ckpt && w == 0) store_f32(p.ckpt + ((int64_t)at.batch * p.tiles + at.time) * p.dim, ch, h);
     if (p.last && w == kTokWarps - 1 && at.time == p.tiles - 1) store_f32(p.last + at.batch * p.dim, ch, out);
     if (p.y) {
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     }
     if (next.id >= total) break;
     at = next.place;
-    __syncthreads();  // every warp is done with the tile's runs
+    if (p.group > 1) __syncthreads();  // every warp is done with the group's runs
   }
 }
 
@@ -418,7 +424,7 @@ template <typename T, bool TIED, bool Z, bool ST>
 __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams p) {
   constexpr int RUN = Tok<T>::RUN, STAGE = kWarpStage<Z, true>;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ TokShared sm;
+  __shared__ TokSharedBwd sm;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned char *ring = smem + w * 2 * STAGE;
   const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
@@ -460,10 +466,8 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
         if ((st >> i) & 1u) R = splat2(0.f);
       }
     }
-    sm.A[w][lane] = r.A;
-    sm.N[w][lane] = r.N;
-    sm.B[w][lane] = R;
-    sm.other[w][lane] = r.B;
+    sm.put(stg, w, lane, {r.A, r.N, R});
+    sm.state[stg][w][lane] = r.B;
     if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
     __syncthreads();
     const Taken next = sm.ticket;
@@ -471,10 +475,10 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     copies_commit();
 #pragma unroll
     for (int i = 0; i < kTokWarps - 1; ++i) {
-      if (i < w) h = run_on2<ST>({sm.A[i][lane], sm.N[i][lane], sm.other[i][lane]}, h);
+      if (i < w) h = run_on2<ST>({sm.A[stg][i][lane], sm.N[stg][i][lane], sm.state[stg][i][lane]}, h);
     }
     f2 out;
-    f2 P = tile_in<ST, true>(p, sm, at.chain, at.time, first, w, lane, q, seen, out);
+    f2 P = tile_in<ST, true>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
     if (p.dh0 && w == 0 && a.time == 0) store_f32(p.dh0 + at.batch * p.dim, ch, out);
     f2 sum = splat2(0.f);
     auto walk = [&](bool all) {
@@ -515,20 +519,19 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     };
     if (p.v32 && a.n == RUN) walk(true);
     else walk(false);
-    __syncthreads();  // every warp is done with the tile's runs
     if (p.dbias_part) {
-      sm.other[w][lane] = sum;
+      sm.sum[w][lane] = sum;
       __syncthreads();
       if (w == 0) {
         f2 t = splat2(0.f);
 #pragma unroll
-        for (int i = 0; i < kTokWarps; ++i) t = add2(t, sm.other[i][lane]);
+        for (int i = 0; i < kTokWarps; ++i) t = add2(t, sm.sum[i][lane]);
         store_f32(p.dbias_part + ((int64_t)at.batch * p.tiles + a.time) * p.dim, ch, t);
       }
     }
     if (next.id >= total) break;
     at = next.place;
-    if (p.dbias_part) __syncthreads();
+    if (p.group > 1) __syncthreads();  // every warp is done with the group's runs
   }
 }
 

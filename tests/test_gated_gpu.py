@@ -171,6 +171,21 @@ def test_long_sequences_cross_many_tiles(cuda_device, path, tok):
 
 
 @pytest.mark.parametrize("path,tok", PATHS)
+@pytest.mark.parametrize("dim", [3, 200])
+def test_outer_states_reach_across_tiles(cuda_device, path, tok, dim):
+    # an initial state and a gradient of the last state far above everything else, under
+    # a long memory (a = 1 - 1e-4): every tile's outputs depend on them
+    def edit(raw, case):
+        raw["f"][:] = 9.0
+    c = Case(cuda_device, 1, dim, 9000, synth.F32, 33, tok=tok, bias=False, edit=edit)
+    for k in ("h0", "dlast"):
+        c.n[k] = c.n[k] * 1000
+        c.t[k].mul_(1000)
+    c.check_fwd(*c.fwd(path))
+    c.check_bwd(c.bwd(path))
+
+
+@pytest.mark.parametrize("path,tok", PATHS)
 def test_many_batches(cuda_device, path, tok):
     c = Case(cuda_device, 70, 11, 90, synth.BF16, 22, tok=tok, starts=0.03)
     c.check_fwd(*c.fwd(path))
