@@ -635,7 +635,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
 constexpr int kRowBwdStages = 2;
 
 template <typename T, bool TIED, bool Z, bool ST, bool FULL>
-__global__ void __launch_bounds__(kRowThreads, 4) k_rows_bwd(GsParams p, int short_lanes) {
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bwd(GsParams p, int short_lanes) {
   using G = Geo<T>;
   const int W = FULL ? 32 : short_lanes;
   extern __shared__ __align__(16) unsigned char smem[];
