@@ -320,9 +320,13 @@ ssm_status ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int
  * channel's sequence in one warp (channel-major only); LOOKBACK splits every
  * sequence into time tiles that hand their states on through the workspace
  * with a bounded wait; AUTO picks; the others return SSM_ERR_UNSUPPORTED.
- * f = +inf leaves the state as it was (a padded step, tied), f = -inf forgets
- * it.  The order of every sum is fixed: repeated calls give equal bits.
- * y may not alias an input.  seqlen 0 copies initial_state to last_state.
+ * With tied gates f = +inf leaves a finite state as it was (a padded step) and
+ * f = -inf forgets it.  Arithmetic and states are fp32; a step rounds relative
+ * to the larger of |h_{t-1}| and |u_t|, and memories of 1e5 steps keep their
+ * length (1 - a is never formed from a).  The order of every sum is fixed:
+ * repeated calls give equal bits.  An infinite state may become NaN.
+ * y may not alias an input; last_state may be initial_state.  seqlen 0 copies
+ * initial_state to last_state.
  *
  * The workspace (256-byte aligned) holds the saved states and the look-back
  * schedule's states; NULL is accepted where the query below gives 0. */
@@ -349,7 +353,7 @@ int32_t ssm_gated_scan_path(const ssm_shape *shape);
  *  dlast_state     [batch][dim] fp32, nullable
  *  du, df, dz      as u, f, z (overwritten); dz exactly when z is given
  *  df_bias         [dim] fp32, exactly when f_bias is given
- *  dinitial_state  [batch][dim] fp32, nullable
+ *  dinitial_state  [batch][dim] fp32, nullable; may be dlast_state
  * No gradient passes a start.  No atomics on results: bitwise repeatable.
  * du, df and dz may not alias an input or one another. */
 ssm_status ssm_gated_scan_bwd(const ssm_shape *shape, const void *u, const void *f,

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kStepThreads) k_gs_step(GsStepParams p) {
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const float ng = -rcp_approx(1.f + ex2(fmaf(fv[k], kLog2e, p.bias ? bv[k] * kLog2e : 0.f)));
-    hv[k] = p.untied ? fmaf(ng, hv[k], hv[k]) + uv[k] : fmaf(ng, hv[k] - uv[k], hv[k]);
+    hv[k] = p.untied ? fmaf(ng, hv[k], hv[k]) + uv[k] : fmaf(ng, -uv[k], fmaf(ng, hv[k], hv[k]));
     o[k] = z ? hv[k] * silu_fast(zv[k]) : hv[k];
   }
   if constexpr (VEC) {

@@ -106,11 +106,14 @@ __device__ __forceinline__ f2 sigmoid2(f2 z) {
   return pack2(rcp_approx(d0), rcp_approx(d1));
 }
 
-// one step of the state: h - g (h - u), or h - g h + u
+// One step of the state: (h - g h) + g u, or (h - g h) + u; `in` is -u where the gates are
+// tied (the sign costs one operation a loaded word), else u.  A gate that rounds to g = 1
+// forgets h whatever its size, which h - g (h - u) would not.
 template <bool TIED>
-__device__ __forceinline__ f2 state_step(f2 h, f2 ng, f2 u) {
-  if constexpr (TIED) return fma2(ng, fma2(u, splat2(-1.f), h), h);
-  return add2(fma2(ng, h, h), u);
+__device__ __forceinline__ f2 state_step(f2 h, f2 ng, f2 in) {
+  const f2 kept = fma2(ng, h, h);
+  if constexpr (TIED) return fma2(ng, in, kept);
+  return add2(kept, in);
 }
 
 // ---- what tiles hand on to one another ----------------------------------------

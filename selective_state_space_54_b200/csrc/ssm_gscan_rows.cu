@@ -42,6 +42,15 @@ __device__ __forceinline__ f2 pair_at(const uint32_t *w, int q) {
   return pack2(at<T>(w, q), at<T>(w, q + Geo<T>::H));
 }
 
+// u as the state's step takes it (see state_step): the signs of a chunk's values turned
+template <typename T, bool TIED>
+__device__ __forceinline__ void as_input(uint32_t (&w)[8]) {
+  if constexpr (TIED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] ^= sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+  }
+}
+
 // ---- a warp's piece of one tensor in shared memory: 32 chunks of 32 bytes -------------
 // The two 16-byte units of a chunk change places in every other group of four lanes, so that
 // eight lanes reading their first (or second) units meet eight different bank groups.
@@ -215,6 +224,7 @@ __device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const unsi
   constexpr int H = Geo<T>::H;
   uint32_t u[8];
   get_chunk(u, stage + kSlotU, lane);
+  as_input<T, TIED>(u);
   f2 A = splat2(1.f), N = splat2(0.f), B = splat2(0.f);
 #pragma unroll
   for (int q = 0; q < H; ++q) {
@@ -277,6 +287,7 @@ __device__ __forceinline__ void lane_out(const GsParams &p, int64_t row, int64_t
   f2 h = pack2(hin, run_on<ST>(lo, hin)), o[H];
   uint32_t u[8], z[8];
   get_chunk(u, stage + kSlotU, lane);
+  as_input<T, TIED>(u);
   if constexpr (Z) get_chunk(z, stage + kSlotZ, lane);
 #pragma unroll
   for (int q = 0; q < H; ++q) {
@@ -381,6 +392,9 @@ __device__ __forceinline__ float look_back(const GsParams &p, int64_t row, unsig
   Run tile = no_run();
 #pragma unroll
   for (int i = 0; i < kGsTileWarps; ++i) tile = join<ST>(runs[FROM_BEHIND ? kGsTileWarps - 1 - i : i], tile);
+  // the row's first tile hands on its state in the place of its run, so that no other tile
+  // reads the state entering the row (which the last one may overwrite)
+  if (c == 0) tile = Run{0.f, -1.f, run_on<ST>(tile, first)};
   if (lane == 0 && !last_in_group) put_run(p.runs + row * p.tiles + c, tile);
   unsigned long long started = 0;
   unsigned n = 0;
@@ -421,8 +435,8 @@ struct TileShared {
 };
 
 // The value entering the warp's own run, after the barrier that shows the warps' runs;
-// FROM_BEHIND: the walk starts at the last warp.  `first` enters the row's first tile; the
-// value leaving the tile is published, and goes to `end` where it leaves the row.  With one
+// FROM_BEHIND: the walk starts at the last warp.  `first` enters the row's first tile (0
+// in the others); the value leaving the tile is published, and goes to `end` where it leaves the row.  With one
 // tile a group every warp reads the state itself and walks the runs before its own; else
 // warp 0 looks back for all.  q, seen: as in look_back (one tile a group: in every warp, the
 // state of the tile before, in every lane).
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     unsigned long long seen;
     const void *q = tile_look(p, row, at.time, seen);
     const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
-    const float first = at.time < p.group && p.h0 ? p.h0[row] : 0.f;
+    const float first = at.time == 0 && p.h0 ? p.h0[row] : 0.f;
     unsigned st = 0;
     if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
     copies_wait<0>();
@@ -592,6 +606,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
     uint32_t f[8], u[8], z[8], g[8];
     get_chunk(f, stage + kSlotF, lane);
     get_chunk(u, stage + kSlotU, lane);
+    as_input<T, TIED>(u);
     if constexpr (Z) {
       get_chunk(z, stage + kSlotZ, lane);
       get_chunk(g, stage + kSlotG<Z>, lane);
@@ -600,7 +615,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
     for (int q = 0; q < H; ++q) {
       if constexpr (ST) h = zero_at(h, (st >> q) & 1u, (st >> (q + H)) & 1u);
       const f2 uv = pair_at<T>(u, q), ag = gate_slope2(pair_at<T>(f, q), b2, ng[q]);
-      wt[q] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
+      wt[q] = mul2(TIED ? add2(h, uv) : h, ag);
       h = state_step<TIED>(h, ng[q], uv);
       if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
         const f2 zv = pair_at<T>(z, q), s = sigmoid2(zv);
@@ -712,7 +727,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     unsigned long long seen;
     const void *q = tile_look(p, row, at.time, seen);
     const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
-    const float first = at.time < p.group && p.dlast ? p.dlast[row] : 0.f;
+    const float first = at.time == 0 && p.dlast ? p.dlast[row] : 0.f;
     const float h0 = chunk >= chunks ? 0.f : chunk > 0 ? p.ckpt[row * chunks + chunk] : (p.h0 ? p.h0[row] : 0.f);
     unsigned st = 0;
     if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);

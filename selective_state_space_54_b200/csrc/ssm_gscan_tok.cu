@@ -44,6 +44,19 @@ __device__ __forceinline__ f2 pair_at(const unsigned char *slot, int i, int lane
   }
 }
 
+// u as the state's step takes it (see state_step)
+template <typename T, bool TIED>
+__device__ __forceinline__ f2 input_at(const unsigned char *slot, int i, int lane) {
+  if constexpr (!TIED) {
+    return pair_at<T>(slot, i, lane);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t v = *reinterpret_cast<const uint32_t *>(slot + i * Tok<T>::ROW + 4 * lane) ^ 0x80008000u;
+    return pack2(bf16_lo(v), bf16_hi(v));
+  } else {
+    return pair_at<T>(slot, i, lane) ^ 0x8000000080000000ull;
+  }
+}
+
 // Copies the warp's steps (n of them, from src: the first one's first channel of the group)
 // into a slot, zeros for steps and channels that are not there.  ch: channels of the group
 // there are.  16-byte pieces (mode 2); out of line, to keep the tile's code short: 4-byte
@@ -257,6 +270,12 @@ __device__ __forceinline__ f2 tile_in(const GsParams &p, TokShared &sm, int cur,
       for (int j = 1; j < kTokWarps; ++j) tile = join2<ST>(sm.of(cur, nth(j), lane), tile);
       Run x, y;
       split(tile, x, y);
+      if (c == 0) {  // the state itself, as in the channel-major form
+        float f0, f1;
+        unpack2(first, f0, f1);
+        x = Run{0.f, -1.f, run_on<ST>(x, f0)};
+        y = Run{0.f, -1.f, run_on<ST>(y, f1)};
+      }
       put_run(runs + (int64_t)c * kTokChannels + 2 * lane, x);
       put_run(runs + (int64_t)c * kTokChannels + 2 * lane + 1, y);
     }
@@ -347,7 +366,7 @@ __device__ __forceinline__ Run2 warp_run(f2 (&ng)[Tok<T>::RUN], const unsigned c
     if constexpr (ST) {
       if ((st >> i) & 1u) r.B = splat2(0.f);
     }
-    r.B = state_step<TIED>(r.B, ng[i], pair_at<T>(stage + kTokU, i, lane));
+    r.B = state_step<TIED>(r.B, ng[i], input_at<T, TIED>(stage + kTokU, i, lane));
     r.N = fma2(ng[i], r.A, r.N);
     r.A = fma2(ng[i], r.A, r.A);
   }
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     const unsigned long long seen = q ? look64(q) : 0ull;
     const Pair ch = {(int64_t)at.rest * kTokChannels + 2 * lane, 2 * lane < a.ch, 2 * lane + 1 < a.ch};
     const f2 b2 = mul2(load_f32(p.bias, ch), splat2(kLog2e));
-    const f2 first = load_f32(p.h0 ? p.h0 + at.batch * p.dim : nullptr, ch);
+    const f2 first = load_f32(p.h0 && at.time == 0 ? p.h0 + at.batch * p.dim : nullptr, ch);
     const unsigned st = warp_starts<T, ST>(p, a.tok, a.n, lane);
     copies_wait<0>();
     __syncwarp();
@@ -401,7 +420,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
           if constexpr (ST) {
             if ((st >> i) & 1u) h = splat2(0.f);
           }
-          h = state_step<TIED>(h, ng[i], pair_at<T>(stage + kTokU, i, lane));
+          h = state_step<TIED>(h, ng[i], input_at<T, TIED>(stage + kTokU, i, lane));
           f2 o = h;
           if constexpr (Z) {
             const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
@@ -445,7 +464,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     const float *hrow = a.time > 0 ? p.ckpt + ((int64_t)at.batch * p.tiles + a.time) * p.dim
                                    : p.h0 ? p.h0 + at.batch * p.dim : nullptr;
     f2 h = load_f32(hrow, ch);
-    const f2 first = load_f32(p.dlast ? p.dlast + at.batch * p.dim : nullptr, ch);
+    const f2 first = load_f32(p.dlast && at.time == 0 ? p.dlast + at.batch * p.dim : nullptr, ch);
     const unsigned st = warp_starts<T, ST>(p, a.tok, a.n, lane);
     copies_wait<0>();
     __syncwarp();
@@ -490,9 +509,9 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
         if constexpr (ST) {
           if ((st >> i) & 1u) h = splat2(0.f);
         }
-        const f2 uv = pair_at<T>(stage + kTokU, i, lane);
+        const f2 uv = input_at<T, TIED>(stage + kTokU, i, lane);
         const f2 ag = gate_slope2(pair_at<T>(stage + kTokF, i, lane), b2, ng[i]);
-        wt[i] = mul2(TIED ? fma2(uv, splat2(-1.f), h) : h, ag);
+        wt[i] = mul2(TIED ? add2(h, uv) : h, ag);
         h = state_step<TIED>(h, ng[i], uv);
         if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
           const f2 zv = pair_at<T>(stage + kTokZ, i, lane), s = sigmoid2(zv);

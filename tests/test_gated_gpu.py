@@ -449,6 +449,43 @@ def test_offsets_past_32_bits(cuda_device, path, tok):
     assert_close(pick(gr["df"]), rb["df"], synth.BF16, "df")
 
 
+@pytest.mark.parametrize("path,tok", PATHS)
+@pytest.mark.parametrize("L", [1, 700, 9000])
+def test_states_in_place(cuda_device, path, tok, L):
+    # last_state over initial_state and dinitial_state over dlast_state, the way a state
+    # is carried along: the same bits as with buffers of their own
+    import torch
+    c = Case(cuda_device, 2, 21, L, synth.BF16, 34, tok=tok, f_mean=8.0)
+    y, last = c.fwd(path)
+    g = c.bwd(path)
+    state, grad = c.t["h0"].clone(), c.t["dlast"].clone()
+    keep = c.t["h0"], c.t["dlast"]
+    c.t["h0"] = state
+    y2, _ = c.fwd(path, last_state=state)
+    c.t["h0"], c.t["dlast"] = keep[0], grad
+    g2 = c.bwd(path, out={"dinitial_state": grad})
+    assert torch.equal(y, y2) and torch.equal(state, last)
+    assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+@pytest.mark.parametrize("path,tok", PATHS)
+def test_a_closed_gate_forgets_any_state(cuda_device, path, tok):
+    # f = -inf (g = 1 exactly): h = u whatever the state before it was, here 2^40 times u
+    import torch
+    import selective_state_space_54_b200 as ssm
+
+    def edit(raw, case):
+        raw["f"][:, :, 0::10] = -np.inf
+        raw["u"][:, :, 5::10] *= 2.0 ** 40
+    c = Case(cuda_device, 1, 12, 600, synth.F32, 35, tok=tok, z=False, bias=False, edit=edit)
+    c.t["h0"].fill_(2.0 ** 60)
+    y, _ = c.fwd(path)
+    assert np.array_equal(c.rows(y)[:, :, 0::10], c.n["u"][:, :, 0::10])
+    state = torch.full((1, 12), 2.0 ** 60, device=cuda_device)
+    one = torch.randn((1, 12), device=cuda_device)
+    assert torch.equal(ssm.gated_scan_step(one, torch.full_like(one, -np.inf), state=state), one)
+
+
 def test_device_and_argument_refusals(cuda_device):
     import torch
     import selective_state_space_54_b200 as ssm
