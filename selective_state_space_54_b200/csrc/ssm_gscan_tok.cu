@@ -406,10 +406,10 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
     __syncthreads();
     const Taken next = sm.ticket;
-    if (next.id < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next.place, w), lane);
-    copies_commit();
     f2 out;
     f2 h = tile_in<ST, false>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
+    if (next.id < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next.place, w), lane);
+    copies_commit();
     if (p.ckpt && w == 0) store_f32(p.ckpt + ((int64_t)at.batch * p.tiles + at.time) * p.dim, ch, h);
     if (p.last && w == kTokWarps - 1 && at.time == p.tiles - 1) store_f32(p.last + at.batch * p.dim, ch, out);
     if (p.y) {
@@ -490,14 +490,14 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
     __syncthreads();
     const Taken next = sm.ticket;
+    f2 out;
+    f2 P = tile_in<ST, true>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
     if (next.id < total) fill_stage<T, Z, true>(ring + (stg ^ 1) * STAGE, p, Where<T, true>(p, next.place, w), lane);
     copies_commit();
 #pragma unroll
     for (int i = 0; i < kTokWarps - 1; ++i) {
       if (i < w) h = run_on2<ST>({sm.A[stg][i][lane], sm.N[stg][i][lane], sm.state[stg][i][lane]}, h);
     }
-    f2 out;
-    f2 P = tile_in<ST, true>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
     if (p.dh0 && w == 0 && a.time == 0) store_f32(p.dh0 + at.batch * p.dim, ch, out);
     f2 sum = splat2(0.f);
     auto walk = [&](bool all) {
