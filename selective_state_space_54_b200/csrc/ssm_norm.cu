@@ -19,6 +19,8 @@
 #include "ssm_layer.cuh"
 
 #include <algorithm>
+#include <initializer_list>
+#include <utility>
 
 namespace ssm {
 
@@ -139,6 +141,84 @@ __device__ __forceinline__ void put8(T *p, const f2 (&o)[4]) {
                  : "memory");
   }
 }
+// ---- rows whose start is not aligned ----------------------------------------------------
+// A row begins `pad` values (0..7) after an aligned place.  Its pieces are the aligned ones,
+// so that its first and last may reach into the neighbouring rows: of those the row's own
+// values [0, dim) are loaded and stored one by one, the others count as 0.  Rows a `period`
+// (8 over the greatest common divisor of 8 and dim) apart have the same pad: a block takes
+// rows of one pad only, and every thread keeps its columns.
+struct Pieces {
+  int period, cls, pad;  // the block's class of rows: row = cls (mod period)
+};
+template <bool SHIFT>
+__device__ __forceinline__ Pieces pieces_of(int period, int base, int64_t dim) {
+  if constexpr (!SHIFT) return {1, 0, 0};
+  const int cls = blockIdx.x % period;
+  return {period, cls, (int)((base + cls * (dim & 7)) & 7)};
+}
+__device__ __forceinline__ bool whole(int i, int dim) { return i >= 0 && i + 8 <= dim; }
+// the piece at column i of row r (the tensor's first value at p)
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void load_piece(Raw8<T> &q, const void *p, int64_t r, int64_t rows, int i, int dim) {
+  const int64_t at = r * dim + i;
+  const T *src = static_cast<const T *>(p) + at;
+  if (!SHIFT || (at >= 0 && at + 8 <= rows * dim)) {
+    load8<T>(q, src);
+  } else {
+#pragma unroll
+    for (int w = 0; w < (int)(8 * sizeof(T) / 4); ++w) q.w[w] = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e >= 0 && i + e < dim) {
+        if constexpr (sizeof(T) == 2) q.w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+        else q.w[e] = __float_as_uint(src[e]);
+      }
+  }
+}
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void put_piece(T *p, const f2 (&o)[4], int i, int dim) {
+  if (!SHIFT || whole(i, dim)) {
+    put8<T>(p, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float a, b;
+      unpack2(o[e >> 1], a, b);
+      if (i + e >= 0 && i + e < dim) IO<T>::store1(p, e, (e & 1) ? b : a);
+    }
+  }
+}
+// the values of a piece that are not the row's, set to 0
+template <bool SHIFT>
+__device__ __forceinline__ void keep_own(f2 (&v)[4], int i, int dim) {
+  if (SHIFT && !whole(i, dim)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a, b;
+      unpack2(v[e], a, b);
+      const int k = i + 2 * e;
+      v[e] = pack2(k >= 0 && k < dim ? a : 0.f, k + 1 >= 0 && k + 1 < dim ? b : 0.f);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void drop_others(Raw8<T> &r, int i, int dim) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (i + e < 0 || i + e >= dim) {
+      if constexpr (sizeof(T) == 2) r.w[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+      else r.w[e] = 0u;
+    }
+}
+// w (and b) moved by pad into shared memory, 0 outside the row, n columns in all
+__device__ __forceinline__ void shift_w(float *to, const float *w, int pad, int dim, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = w && i >= pad && i - pad < dim ? w[i - pad] : 0.f;
+}
+__device__ __forceinline__ void get_w_shared(const float *p, f2 (&o)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p), b = *(reinterpret_cast<const ulonglong2 *>(p) + 1);
+  o[0] = a.x; o[1] = a.y; o[2] = b.x; o[3] = b.y;
+}
+
 // 8 fp32 parameters as pairs
 __device__ __forceinline__ void get_w(const float *p, f2 (&o)[4]) {
   const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2 *>(p)), b = __ldg(reinterpret_cast<const ulonglong2 *>(p) + 1);
@@ -159,14 +239,22 @@ __device__ __forceinline__ float both(f2 v) {
 // ---- forward ------------------------------------------------------------------------
 // NV pieces of 8 values per thread and row, RB rows at a time, wpr warps a row; a block
 // holds blockDim / (32 wpr) such groups.  Q as in row_sums; MAXT threads, MINB blocks an SM.
-template <typename T, typename R, bool RES, int NV, int RB, int Q, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr) {
+template <typename T, typename R, bool RES, int NV, int RB, int Q, int MAXT, int MINB, bool SHIFT>
+__global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr, int period, int pad0) {
+  extern __shared__ __align__(16) float shifted[];  // SHIFT: w, then b
   __shared__ RowSums red[2];
   const int tpr = 32 * wpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
   const int dim = (int)p.dim;
   const float inv = 1.f / (float)dim;
-  const int64_t step = (int64_t)gridDim.x * groups * RB;
-  int64_t row = ((int64_t)blockIdx.x * groups + group) * RB;
+  const Pieces pc = pieces_of<SHIFT>(period, pad0, p.dim);
+  const int per = pc.period, pad = pc.pad, cols = 8 * NV * tpr;
+  // rows cls, cls + per, ..: RB of them at a time from `row`
+  const int64_t step = (int64_t)(gridDim.x / per) * groups * RB * per;
+  int64_t row = ((int64_t)(blockIdx.x / per) * groups + group) * RB * per + pc.cls;
+  if constexpr (SHIFT) {
+    shift_w(shifted, p.w, pad, dim, cols);
+    shift_w(shifted + cols, p.b, pad, dim, cols);
+  }
   Raw8<T> x[RB][NV];
   Raw8<R> a[RES ? RB : 1][NV];
   auto load = [&](int64_t r) {
@@ -174,10 +262,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
     for (int j = 0; j < RB; ++j) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int i = (k * tpr + tid) * 8;
-        if (r + j < p.rows && i < dim) {
-          load8<T>(x[j][k], static_cast<const T *>(p.x) + (r + j) * p.dim + i);
-          if constexpr (RES) load8<R>(a[j][k], static_cast<const R *>(p.res) + (r + j) * p.dim + i);
+        const int i = (k * tpr + tid) * 8 - pad;
+        if (r + j * per < p.rows && i < dim) {
+          load_piece<T, SHIFT>(x[j][k], p.x, r + j * per, p.rows, i, dim);
+          if constexpr (RES) load_piece<R, SHIFT>(a[j][k], p.res, r + j * per, p.rows, i, dim);
         }
       }
     }
@@ -187,7 +275,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
   clear(red[1]);
   __syncthreads();
   // every group of the block takes the same rounds (barriers in row_sums)
-  for (int64_t r0 = (int64_t)blockIdx.x * groups * RB; r0 < p.rows; r0 += step, row += step) {
+  for (int64_t r0 = (int64_t)(blockIdx.x / per) * groups * RB * per + pc.cls; r0 < p.rows; r0 += step, row += step) {
     f2 v[RB][NV][4];
     float sum[RB], sq[RB];
 #pragma unroll
@@ -195,8 +283,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
       f2 t = splat2(0.f);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int i = (k * tpr + tid) * 8;
-        if (row + j >= p.rows || i >= dim) continue;
+        const int i = (k * tpr + tid) * 8 - pad;
+        if (row + j * per >= p.rows || i >= dim) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][k][e] = pair_of<T>(x[j][k], e);
         if constexpr (RES) {
@@ -205,8 +293,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
             v[j][k][e] = add2(v[j][k][e], pair_of<R>(a[j][k], e));
             if constexpr (sizeof(R) == 2) v[j][k][e] = stored_bf16(v[j][k][e]);
           }
-          put8<R>(static_cast<R *>(p.res_out) + (row + j) * p.dim + i, v[j][k]);
+          put_piece<R, SHIFT>(static_cast<R *>(p.res_out) + (row + j * per) * p.dim + i, v[j][k], i, dim);
         }
+        keep_own<SHIFT>(v[j][k], i, dim);
         t = add2(t, add2(add2(v[j][k][0], v[j][k][1]), add2(v[j][k][2], v[j][k][3])));
       }
       sum[j] = both(t);
@@ -219,12 +308,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
       f2 t = splat2(0.f);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (row + j >= p.rows || (k * tpr + tid) * 8 >= dim) continue;
+        if (row + j * per >= p.rows || (k * tpr + tid) * 8 - pad >= dim) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[j][k][e] = add2(v[j][k][e], m);
-          t = fma2(v[j][k][e], v[j][k][e], t);
-        }
+        for (int e = 0; e < 4; ++e) v[j][k][e] = add2(v[j][k][e], m);
+        keep_own<SHIFT>(v[j][k], (k * tpr + tid) * 8 - pad, dim);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t = fma2(v[j][k][e], v[j][k][e], t);
       }
       sq[j] = both(t);
     }
@@ -233,19 +322,24 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_rows(NormParams p, int wpr)
     for (int j = 0; j < RB; ++j) sq[j] = rsqrtf(fmaf(sq[j], inv, p.eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * 8;
+      const int i = (k * tpr + tid) * 8 - pad;
       if (i >= dim) continue;
       f2 w[4], b[4];
-      get_w(p.w + i, w);
+      if constexpr (SHIFT) {
+        get_w_shared(shifted + i + pad, w);
+        get_w_shared(shifted + cols + i + pad, b);
+      } else {
+        get_w(p.w + i, w);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = splat2(0.f);
-      if (p.b) get_w(p.b + i, b);
+        for (int e = 0; e < 4; ++e) b[e] = splat2(0.f);
+        if (p.b) get_w(p.b + i, b);
+      }
 #pragma unroll
       for (int j = 0; j < RB; ++j) {
-        if (row + j >= p.rows) continue;
+        if (row + j * per >= p.rows) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][k][e] = fma2(mul2(v[j][k][e], splat2(sq[j])), w[e], b[e]);
-        put8<T>(static_cast<T *>(p.y) + (row + j) * p.dim + i, v[j][k]);
+        put_piece<T, SHIFT>(static_cast<T *>(p.y) + (row + j * per) * p.dim + i, v[j][k], i, dim);
       }
     }
   }
@@ -391,25 +485,29 @@ __device__ __forceinline__ void block_part(float *acc, float v, int tpr, int rpb
   if (in) *out = v;
 }
 
-template <typename T, typename R, bool DRO, int NV, int Q, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, int wpr) {
+template <typename T, typename R, bool DRO, int NV, int Q, int MAXT, int MINB, bool SHIFT>
+__global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, int wpr, int period, int pad0) {
+  extern __shared__ __align__(16) float shifted[];  // SHIFT: w
   __shared__ RowSums red[2];
   __shared__ float acc[MAXT];
   const int tpr = 32 * wpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
   const int dim = (int)p.dim;
   const float inv = 1.f / (float)dim;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + group;
+  const Pieces pc = pieces_of<SHIFT>(period, pad0, p.dim);
+  const int per = pc.period, pad = pc.pad;
+  const int64_t step = (int64_t)(gridDim.x / per) * groups * per;
+  int64_t row = ((int64_t)(blockIdx.x / per) * groups + group) * per + pc.cls;
+  if constexpr (SHIFT) shift_w(shifted, p.w, pad, dim, 8 * NV * tpr);
   Raw8<R> s[NV], dro[DRO ? NV : 1];
   Raw8<T> d[NV];
   auto load = [&](int64_t r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * 8;
+      const int i = (k * tpr + tid) * 8 - pad;
       if (r < p.rows && i < dim) {
-        load8<R>(s[k], static_cast<const R *>(p.s) + r * p.dim + i);
-        load8<T>(d[k], static_cast<const T *>(p.dy) + r * p.dim + i);
-        if constexpr (DRO) load8<R>(dro[k], static_cast<const R *>(p.dres_out) + r * p.dim + i);
+        load_piece<R, SHIFT>(s[k], p.s, r, p.rows, i, dim);
+        load_piece<T, SHIFT>(d[k], p.dy, r, p.rows, i, dim);
+        if constexpr (DRO) load_piece<R, SHIFT>(dro[k], p.dres_out, r, p.rows, i, dim);
       }
     }
   };
@@ -423,19 +521,21 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
   clear(red[0]);
   clear(red[1]);
   __syncthreads();
-  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, row += step) {
+  for (int64_t r0 = (int64_t)(blockIdx.x / per) * groups * per + pc.cls; r0 < p.rows; r0 += step, row += step) {
     const bool live = row < p.rows;
     f2 c[NV][4], t = splat2(0.f);
     Raw8<T> g[NV];
     Raw8<R> o[DRO ? NV : 1];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * 8;
+      const int i = (k * tpr + tid) * 8 - pad;
       if (!live || i >= dim) continue;
       if constexpr (DRO) o[k] = dro[k];
       g[k] = d[k];
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[k][e] = pair_of<R>(s[k], e);
+      keep_own<SHIFT>(c[k], i, dim);
+      if (SHIFT && !whole(i, dim)) drop_others<T>(g[k], i, dim);
       t = add2(t, add2(add2(c[k][0], c[k][1]), add2(c[k][2], c[k][3])));
     }
     load(row + step);
@@ -445,13 +545,16 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
     f2 a0 = splat2(0.f), a1 = splat2(0.f), a2 = splat2(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * 8;
+      const int i = (k * tpr + tid) * 8 - pad;
       if (!live || i >= dim) continue;
       f2 w[4];
-      get_w(p.w + i, w);
+      if constexpr (SHIFT) get_w_shared(shifted + i + pad, w);
+      else get_w(p.w + i, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[k][e] = add2(c[k][e], m);
+      keep_own<SHIFT>(c[k], i, dim);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        c[k][e] = add2(c[k][e], m);
         const f2 wd = mul2(w[e], pair_of<T>(g[k], e));
         a0 = fma2(c[k][e], c[k][e], a0);
         a1 = fma2(wd, c[k][e], a1);
@@ -464,10 +567,11 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
     const f2 r2 = splat2(r), k1 = splat2(-(s3[1] * inv * r)), k2 = splat2(-(s3[2] * inv));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = (k * tpr + tid) * 8;
+      const int i = (k * tpr + tid) * 8 - pad;
       if (!live || i >= dim) continue;
       f2 w[4], v[4];
-      get_w(p.w + i, w);
+      if constexpr (SHIFT) get_w_shared(shifted + i + pad, w);
+      else get_w(p.w + i, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const f2 q = mul2(c[k][e], r2), gd = pair_of<T>(g[k], e);
@@ -477,8 +581,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
         if constexpr (DRO) v[e] = fma2(r2, ds, pair_of<R>(o[k], e));
         else v[e] = mul2(r2, ds);
       }
-      put8<T>(static_cast<T *>(p.dx) + row * p.dim + i, v);
-      if constexpr (sizeof(R) != sizeof(T)) put8<R>(static_cast<R *>(p.dres) + row * p.dim + i, v);
+      put_piece<T, SHIFT>(static_cast<T *>(p.dx) + row * p.dim + i, v, i, dim);
+      if constexpr (sizeof(R) != sizeof(T)) put_piece<R, SHIFT>(static_cast<R *>(p.dres) + row * p.dim + i, v, i, dim);
     }
   }
   float *part = p.part + (int64_t)blockIdx.x * 2 * p.dim;  // [block][2][dim]
@@ -486,13 +590,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_bwd_rows(NormBwdParams p, i
   for (int k = 0; k < NV; ++k) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = (k * tpr + tid) * 8 + 2 * e;
+      const int i = (k * tpr + tid) * 8 - pad + 2 * e;
       float v[4];
       unpack2(dw[k][e], v[0], v[1]);
       unpack2(db[k][e], v[2], v[3]);
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        block_part(acc, v[h], tpr, groups, part + (h >> 1) * p.dim + i + (h & 1), i < dim);
+        block_part(acc, v[h], tpr, groups, part + (h >> 1) * p.dim + i + (h & 1),
+                        i + (h & 1) >= 0 && i + (h & 1) < dim);
     }
   }
 }
@@ -675,11 +780,29 @@ __global__ void __launch_bounds__(1024) k_norm_sum(const float *part, float *dw,
 }
 
 // ---- launches -----------------------------------------------------------------------
-bool a32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kWidest = 16384;     // columns that 16 warps hold at 32 values a thread
 constexpr int kWidestBwd = 8192;   // backward, 16 values a thread beside their sums
+
+// How rows are cut into pieces of 8 values: aligned (period 0), or moved.  The tensors of a
+// call have to be off by the same number of values.
+struct Cut {
+  bool ok;
+  int period, pad;
+};
+Cut cut_of(int64_t dim, std::initializer_list<std::pair<const void *, size_t>> tensors) {
+  int pad = -1;
+  for (const auto &t : tensors) {
+    if (!t.first) continue;
+    const int q = (int)(reinterpret_cast<uintptr_t>(t.first) / t.second % 8);
+    if (pad >= 0 && q != pad) return {false, 0, 0};
+    pad = q;
+  }
+  if (pad == 0 && dim % 8 == 0) return {true, 0, 0};
+  if (dim < 8) return {false, 0, 0};  // not one piece: columns one by one
+  return {true, dim % 8 == 0 ? 1 : dim % 4 == 0 ? 2 : dim % 2 == 0 ? 4 : 8, pad};
+}
 
 // Warps a row and pieces of 8 values a thread: up to 2048 columns 1, 2 or 4 warps (blocks
 // of 8 warps hold several rows), above that a block a row, as many warps as 16 values a
@@ -703,44 +826,72 @@ RowShape row_shape(int64_t dim, int64_t rows, int sms) {
   return r;
 }
 
+// a grid of at most `most` blocks for `need`, in whole periods
+unsigned grid_of(int64_t need, int64_t most, int period) {
+  const int64_t n = std::max<int64_t>(1, std::min(need, most));
+  return (unsigned)(period <= 1 ? n : std::max<int64_t>(period, n / period * period));
+}
+
+template <typename K>
+cudaError_t with_smem(K kern, int smem) {
+  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+}
+
+// Forward rows that are not aligned go in moved pieces where every tensor is bf16 (5000 x
+// 1001 with a residual: 16.6 us, column by column 20.7) and column by column, whose 4-byte
+// accesses are full-width already, where one is fp32 (5000 x 4001: 58 us, moved 73).  The
+// backward, with more tensors to a column, always goes in moved pieces (85 us against 94).
+template <typename T, typename R, bool RES>
+constexpr bool kMoved = sizeof(T) == 2 && (!RES || sizeof(R) == 2);
+
 template <typename T, typename R, bool RES, int NV, int RB, int Q, int MAXT, int MINB>
-cudaError_t norm_rows(const NormParams &p, const RowShape &sh, int sms, cudaStream_t s) {
+cudaError_t norm_rows(const NormParams &p, const Cut &c, const RowShape &sh, int sms, cudaStream_t s) {
   const int rows = RB * (sh.threads / (32 * sh.wpr));  // a block's at a time
   const int64_t need = (p.rows + rows - 1) / rows, fit = (int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads);
-  k_norm_rows<T, R, RES, NV, RB, Q, MAXT, MINB><<<(unsigned)std::min(need, fit), sh.threads, 0, s>>>(p, sh.wpr);
+  const unsigned grid = grid_of(need, fit, c.period);
+  if (c.period == 0) {
+    k_norm_rows<T, R, RES, NV, RB, Q, MAXT, MINB, false><<<grid, sh.threads, 0, s>>>(p, sh.wpr, 0, 0);
+  } else if constexpr (kMoved<T, R, RES>) {
+    const int smem = 2 * 4 * 256 * NV * sh.wpr;
+    auto kern = k_norm_rows<T, R, RES, NV, RB, Q, MAXT, MINB, true>;
+    const cudaError_t e = with_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, sh.threads, smem, s>>>(p, sh.wpr, c.period, c.pad);
+  }
   return cudaGetLastError();
 }
 
 template <typename T, typename R, bool RES>
-cudaError_t norm_vec(const NormParams &p, int sms, cudaStream_t s) {
-  RowShape sh = row_shape(p.dim, p.rows, sms);
+cudaError_t norm_vec(const NormParams &p, const Cut &c, int sms, cudaStream_t s) {
+  const int64_t dim = p.dim + (c.period ? 7 : 0);  // columns the pieces reach over
+  RowShape sh = row_shape(dim, p.rows, sms);
   constexpr int BYTES = (int)sizeof(T) + (RES ? (int)sizeof(R) : 0);
   if constexpr (BYTES <= 2) {
     // bf16 alone is bound by instructions as much as by memory: 32 values a thread, of one
     // row or of several, in blocks of 4 warps (16384 columns: 16).  Measured at 32768 x 4096:
     // 105 us; 109 us with 2 rows of 16 values in blocks of 8 warps, 118 us with one.
-    if (p.rows * ((p.dim + 1023) / 1024) >= 8 * (int64_t)sms) {
-      sh.nv = p.dim <= 256 ? 1 : p.dim <= 512 ? 2 : 4;
-      sh.wpr = (int)((p.dim + 256 * sh.nv - 1) / (256 * sh.nv));
+    if (p.rows * ((dim + 1023) / 1024) >= 8 * (int64_t)sms) {
+      sh.nv = dim <= 256 ? 1 : dim <= 512 ? 2 : 4;
+      sh.wpr = (int)((dim + 256 * sh.nv - 1) / (256 * sh.nv));
       sh.threads = sh.wpr == 1 || sh.wpr == 2 ? 128 : 32 * sh.wpr;
-      if (sh.nv == 1) return norm_rows<T, R, RES, 1, 4, 1, 128, 4>(p, sh, sms, s);
-      if (sh.nv == 2) return norm_rows<T, R, RES, 2, 2, 1, 128, 4>(p, sh, sms, s);
-      if (sh.threads <= 128) return norm_rows<T, R, RES, 4, 1, 1, 128, 4>(p, sh, sms, s);
-      if (sh.threads <= 256) return norm_rows<T, R, RES, 4, 1, 2, 256, 2>(p, sh, sms, s);
-      return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, sh, sms, s);
+      if (sh.nv == 1) return norm_rows<T, R, RES, 1, 4, 1, 128, 4>(p, c, sh, sms, s);
+      if (sh.nv == 2) return norm_rows<T, R, RES, 2, 2, 1, 128, 4>(p, c, sh, sms, s);
+      if (sh.threads <= 128) return norm_rows<T, R, RES, 4, 1, 1, 128, 4>(p, c, sh, sms, s);
+      if (sh.threads <= 256) return norm_rows<T, R, RES, 4, 1, 2, 256, 2>(p, c, sh, sms, s);
+      return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, c, sh, sms, s);
     }
   }
   // two rows at a time while the next rows' registers (4 a piece in bf16, 8 in fp32) allow
   constexpr int RB = BYTES <= 6 ? 2 : 1;
   if (sh.nv == 1) {
-    if (sh.threads <= 256) return norm_rows<T, R, RES, 1, RB, 2, 256, RB == 2 ? 3 : 4>(p, sh, sms, s);
-    return norm_rows<T, R, RES, 1, 1, 4, 512, 2>(p, sh, sms, s);
+    if (sh.threads <= 256) return norm_rows<T, R, RES, 1, RB, 2, 256, RB == 2 ? 3 : 4>(p, c, sh, sms, s);
+    return norm_rows<T, R, RES, 1, 1, 4, 512, 2>(p, c, sh, sms, s);
   }
   if (sh.nv == 2) {
-    if (sh.threads <= 256) return norm_rows<T, R, RES, 2, RB, 2, 256, 2>(p, sh, sms, s);
-    return norm_rows<T, R, RES, 2, 1, 4, 512, 1>(p, sh, sms, s);
+    if (sh.threads <= 256) return norm_rows<T, R, RES, 2, RB, 2, 256, 2>(p, c, sh, sms, s);
+    return norm_rows<T, R, RES, 2, 1, 4, 512, 1>(p, c, sh, sms, s);
   }
-  return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, sh, sms, s);
+  return norm_rows<T, R, RES, 4, 1, 4, 512, 1>(p, c, sh, sms, s);
 }
 
 // Columns one by one: 8 a thread up to 4096 columns, 16 and 32 beyond.
@@ -775,20 +926,21 @@ cudaError_t norm_scalar(const NormParams &p, int sms, cudaStream_t s) {
 
 template <typename T, typename R>
 cudaError_t norm_t(const NormParams &p, int sms, cudaStream_t s) {
-  auto at = [](const void *q, size_t es) { return es == 4 ? a32(q) : a16(q); };  // 8 values
-  const bool vec = p.dim % 8 == 0 && at(p.x, sizeof(T)) && at(p.res, sizeof(R)) && at(p.y, sizeof(T)) &&
-                   at(p.res_out, sizeof(R)) && a16(p.w) && a16(p.b);
+  const Cut c = cut_of(p.dim, {{p.x, sizeof(T)}, {p.res, sizeof(R)}, {p.y, sizeof(T)}, {p.res_out, sizeof(R)}});
+  const bool vec = c.ok && c.period == 0 && a16(p.w) && a16(p.b);
   if (p.dim > kWidest) {
     if (vec) k_norm_wide<T, R, 8><<<(unsigned)p.rows, kWideThreads, 0, s>>>(p);
     else k_norm_wide<T, R, 1><<<(unsigned)p.rows, kWideThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  if (vec) return p.res ? norm_vec<T, R, true>(p, sms, s) : norm_vec<T, R, false>(p, sms, s);
+  const bool moved = c.ok && c.period && p.dim + 7 <= kWidest;
+  if (p.res ? vec || (moved && kMoved<T, R, true>) : vec || (moved && kMoved<T, R, false>))
+    return p.res ? norm_vec<T, R, true>(p, c, sms, s) : norm_vec<T, R, false>(p, c, sms, s);
   return p.res ? norm_scalar<T, R, true>(p, sms, s) : norm_scalar<T, R, false>(p, sms, s);
 }
 
 // blocks of the backward: enough to fill the machine, no more than there are rows
-int64_t bwd_blocks_for(int64_t rows, int sms) { return std::max<int64_t>(1, std::min<int64_t>(rows, 3 * (int64_t)sms)); }
+int64_t bwd_blocks_for(int64_t rows, int sms) { return std::max<int64_t>(8, std::min<int64_t>(rows, 3 * (int64_t)sms)); }
 
 cudaError_t norm_parts(const NormBwdParams &p, int64_t blocks, cudaStream_t s) {
   k_norm_sum<<<(unsigned)(((p.db ? 2 : 1) * p.dim + 31) / 32), dim3(32, 32), 0, s>>>(p.part, p.dw, p.db, blocks, p.dim);
@@ -796,24 +948,33 @@ cudaError_t norm_parts(const NormBwdParams &p, int64_t blocks, cudaStream_t s) {
 }
 
 template <typename T, typename R, bool DRO, int NV, int Q, int MAXT, int MINB>
-cudaError_t bwd_rows(const NormBwdParams &p, const RowShape &sh, int sms, cudaStream_t s) {
+cudaError_t bwd_rows(const NormBwdParams &p, const Cut &c, const RowShape &sh, int sms, cudaStream_t s) {
   const int groups = sh.threads / (32 * sh.wpr);
-  const int64_t fit = (int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads);
-  const int64_t blocks = std::min(std::min((p.rows + groups - 1) / groups, fit), bwd_blocks_for(p.rows, sms));
-  k_norm_bwd_rows<T, R, DRO, NV, Q, MAXT, MINB><<<(unsigned)blocks, sh.threads, 0, s>>>(p, sh.wpr);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : norm_parts(p, blocks, s);
+  const int64_t fit = std::min<int64_t>((int64_t)sms * std::max(MINB, MAXT * MINB / sh.threads), bwd_blocks_for(p.rows, sms));
+  const unsigned grid = grid_of((p.rows + groups - 1) / groups, fit, c.period);
+  cudaError_t e;
+  if (c.period == 0) {
+    k_norm_bwd_rows<T, R, DRO, NV, Q, MAXT, MINB, false><<<grid, sh.threads, 0, s>>>(p, sh.wpr, 0, 0);
+  } else {
+    const int smem = 4 * 256 * NV * sh.wpr;
+    auto kern = k_norm_bwd_rows<T, R, DRO, NV, Q, MAXT, MINB, true>;
+    if ((e = with_smem(kern, smem)) != cudaSuccess) return e;
+    kern<<<grid, sh.threads, smem, s>>>(p, sh.wpr, c.period, c.pad);
+  }
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : norm_parts(p, grid, s);
 }
 
 template <typename T, typename R, bool DRO>
-cudaError_t bwd_vec(const NormBwdParams &p, int sms, cudaStream_t s) {
-  RowShape sh = row_shape(p.dim, p.rows, sms);
+cudaError_t bwd_vec(const NormBwdParams &p, const Cut &c, int sms, cudaStream_t s) {
+  const int64_t dim = p.dim + (c.period ? 7 : 0);
+  RowShape sh = row_shape(dim, p.rows, sms);
   // with the residual's gradient on an fp32 stream a third tensor waits in registers: 8
   // values a thread up to 4096 columns (16384 x 4096: 192 us, 261 us with 16)
   constexpr bool WIDE = DRO && sizeof(R) == 4;
-  if (WIDE && p.dim <= 4096) {
+  if (WIDE && dim <= 4096) {
     sh.nv = 1;
-    sh.wpr = (int)((p.dim + 255) / 256);
+    sh.wpr = (int)((dim + 255) / 256);
     if (sh.wpr <= 4) {
       while (sh.wpr & (sh.wpr - 1)) ++sh.wpr;
       sh.threads = 256;
@@ -822,14 +983,14 @@ cudaError_t bwd_vec(const NormBwdParams &p, int sms, cudaStream_t s) {
     }
   }
   if (sh.nv == 1) {
-    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, WIDE ? 2 : 3>(p, sh, sms, s);
-    return bwd_rows<T, R, DRO, 1, 4, 512, 1>(p, sh, sms, s);
+    if (sh.threads <= 256) return bwd_rows<T, R, DRO, 1, 2, 256, WIDE ? 2 : 3>(p, c, sh, sms, s);
+    return bwd_rows<T, R, DRO, 1, 4, 512, 1>(p, c, sh, sms, s);
   }
-  if (sh.threads <= 256) return bwd_rows<T, R, DRO, 2, 2, 256, WIDE ? 1 : 2>(p, sh, sms, s);
+  if (sh.threads <= 256) return bwd_rows<T, R, DRO, 2, 2, 256, WIDE ? 1 : 2>(p, c, sh, sms, s);
   if constexpr (WIDE) {  // 204 registers a thread: none spills
-    if (sh.threads <= 320) return bwd_rows<T, R, DRO, 2, 4, 320, 1>(p, sh, sms, s);
+    if (sh.threads <= 320) return bwd_rows<T, R, DRO, 2, 4, 320, 1>(p, c, sh, sms, s);
   }
-  return bwd_rows<T, R, DRO, 2, 4, 512, 1>(p, sh, sms, s);
+  return bwd_rows<T, R, DRO, 2, 4, 512, 1>(p, c, sh, sms, s);
 }
 
 template <typename T, typename R, bool DRO, int NV, int MAXT, int MINB>
@@ -852,10 +1013,10 @@ cudaError_t bwd_scalar(const NormBwdParams &p, int sms, cudaStream_t s) {
 
 template <typename T, typename R>
 cudaError_t norm_bwd_t(const NormBwdParams &p, int sms, cudaStream_t s) {
-  auto at = [](const void *q, size_t es) { return es == 4 ? a32(q) : a16(q); };  // 8 values
-  const bool vec = p.dim % 8 == 0 && at(p.s, sizeof(R)) && at(p.dy, sizeof(T)) && at(p.dres_out, sizeof(R)) &&
-                   at(p.dx, sizeof(T)) && at(p.dres, sizeof(R)) && a16(p.w);
-  if (vec && p.dim <= kWidestBwd) return p.dres_out ? bwd_vec<T, R, true>(p, sms, s) : bwd_vec<T, R, false>(p, sms, s);
+  const Cut c = cut_of(p.dim, {{p.s, sizeof(R)}, {p.dy, sizeof(T)}, {p.dres_out, sizeof(R)}, {p.dx, sizeof(T)}, {p.dres, sizeof(R)}});
+  const bool vec = c.ok && c.period == 0 && a16(p.w);
+  if ((vec && p.dim <= kWidestBwd) || (c.ok && c.period && p.dim + 7 <= kWidestBwd))
+    return p.dres_out ? bwd_vec<T, R, true>(p, c, sms, s) : bwd_vec<T, R, false>(p, c, sms, s);
   if (p.dim > kWidestBwd) {
     const int64_t splits = bwd_blocks_for((p.rows + 31) / 32, sms);
     float2 *stats = reinterpret_cast<float2 *>(p.part + splits * 2 * p.dim);
