@@ -514,3 +514,15 @@ def test_device_and_argument_refusals(cuda_device):
         ssm.gated_scan_bwd(u, u, None, None, u, fwd_workspace=torch.empty(16, dtype=torch.uint8, device=cuda_device))
     with pytest.raises(ValueError):
         ssm.gated_scan_step(u[:, :, 0], u[:, :, 0], state=torch.zeros((2, 8), device=cuda_device))  # strided
+
+
+@pytest.mark.parametrize("shape", [(0, 8, 16), (2, 0, 16), (2, 8, 0), (0, 0, 0)])
+@pytest.mark.parametrize("token_major", [False, True])
+def test_queries_of_empty_shapes(cuda_device, shape, token_major):
+    import torch
+    import selective_state_space_54_b200 as ssm
+    u = torch.zeros(shape, device=cuda_device)
+    for path in (ssm.SSM_PATH_AUTO, ssm.SSM_PATH_LOOKBACK):
+        sh = ssm.gated_scan_shape(u, token_major=token_major, path=path)
+        assert ssm.gated_scan_fwd_workspace_bytes(sh) == 0 and ssm.gated_scan_bwd_workspace_bytes(sh) == 0
+        assert ssm.gated_scan_path(sh) in ssm.PATH_NAMES.values()
