@@ -644,6 +644,9 @@ def layer_norm_bwd(s, weight, bias, dy, *, eps=1e-5, dresidual_out=None, out=Non
         _check_io(name, t, shp, ty, dev)
     lib = _lib.load()
     given = out or {}
+    for name, wanted in (("dresidual", io != rd), ("dbias", bias is not None)):
+        if not wanted and given.get(name) is not None:
+            raise ValueError(f"out holds {name}, which this call has no use for")
 
     def gradient(name, wanted, shp, ty):
         if wanted and given.get(name) is not None:

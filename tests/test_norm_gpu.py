@@ -258,3 +258,13 @@ def test_refusals(cuda_device):
         ssm.layer_norm_bwd(x, w, None, x.float())
     with pytest.raises(ssm.ScanError):
         ssm.layer_norm_bwd(x, w, None, x, out={"dx": x})
+
+
+def test_gradients_that_are_not_formed_are_refused(cuda_device):
+    import torch
+    import selective_state_space_54_b200 as ssm
+    x, w = torch.ones((4, 16), device=cuda_device), torch.ones(16, device=cuda_device)
+    with pytest.raises(ValueError):  # the residual's gradient is dx itself
+        ssm.layer_norm_bwd(x, w, w, x, out={"dresidual": torch.empty_like(x)})
+    with pytest.raises(ValueError):
+        ssm.layer_norm_bwd(x, w, None, x, out={"dbias": torch.empty_like(w)})
