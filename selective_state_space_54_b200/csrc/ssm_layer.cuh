@@ -45,8 +45,8 @@ struct GsParams {
   int64_t batch, dim, L;
   int tok, untied;
   int vec;                           // accesses rows allow: 2 = 16 bytes, 1 = 4, 0 = one element
-  int v32;                           // channel-major: 32-byte stores
-  int start_vec;                     // starts rows 16-byte aligned
+  int v32;                           // channel-major: 32-byte stores; token-major: two channels at once
+  int start_vec;                     // starts rows 4-byte aligned
   // look-back schedule (zeroed): error word, ticket counter, tile runs, group states
   unsigned *err, *ticket;
   unsigned long long *runs;

@@ -15,7 +15,9 @@
 // two rows at a time where the registers allow.  Measured and dropped: rows copied ahead by
 // cp.async (16-byte copies of fp32 rows read every sector twice: 170 against 136 us at
 // 16384 x 4096 on an fp32 residual), w and b read from L1 for every single row (L1 at 70 %).
-// Rows wider than 16384 take walks over memory.
+// Rows wider than 16384 (backward 8192) take walks over memory.  Forward and backward of the
+// measured copy rate (6.46 TB/s): 32768 x 4096 bf16 105 us, 79 %; 16384 x 4096 bf16 on an
+// fp32 residual 330 us, 88 % of the 291 us that the two calls' own accesses take.
 #include "ssm_layer.cuh"
 
 #include <algorithm>
@@ -26,8 +28,8 @@ namespace ssm {
 
 namespace {
 
-// w and b: read by every row, kept in L1
-// VEC values at i: 16-byte accesses for 8, element accesses for 1
+// VEC values at i, 16-byte accesses for 8 and element accesses for 1: w and b, which every
+// row reads
 template <int VEC>
 __device__ __forceinline__ void load_w(const float *p, int64_t i, float (&o)[VEC]) {
   if constexpr (VEC == 1) o[0] = __ldg(p + i);
@@ -143,8 +145,9 @@ __device__ __forceinline__ void put8(T *p, const f2 (&o)[4]) {
 }
 // ---- rows whose start is not aligned ----------------------------------------------------
 // A row begins `pad` values (0..7) after an aligned place.  Its pieces are the aligned ones,
-// so that its first and last may reach into the neighbouring rows: of those the row's own
-// values [0, dim) are loaded and stored one by one, the others count as 0.  Rows a `period`
+// so that its first and last may reach into the neighbouring rows: they are loaded whole (one by
+// one only at the tensor's own ends), what is not the row's counts as 0, and only the row's
+// own values are stored.  Rows a `period`
 // (8 over the greatest common divisor of 8 and dim) apart have the same pad: a block takes
 // rows of one pad only, and every thread keeps its columns.
 struct Pieces {
@@ -461,9 +464,10 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormParams p) {
 
 // ---- backward -----------------------------------------------------------------------
 // Blocks walk the rows, wpr warps a row, each thread on the same columns of every row,
-// whose dw and db it sums in registers.  The block's sums go to the workspace and k_norm_sum adds them in a fixed order.  w dy is rounded once and the
-// same wherever it is used (no contraction into the sums): a row whose terms cancel, such
-// as one of a single column, cancels exactly.
+// whose dw and db it sums in registers.  The block's sums go to the workspace and k_norm_sum
+// adds them in a fixed order.  Rows column by column (all those of fewer than 8 columns):
+// w dy is rounded once and the same wherever it is used (no contraction into the sums), so
+// that a row whose terms cancel, such as one of a single column, cancels exactly.
 __device__ __forceinline__ void grad_terms(float c, float g, float w, float (&s3)[3]) {
   const float wd = __fmul_rn(w, g);
   s3[0] = fmaf(c, c, s3[0]);
@@ -895,7 +899,7 @@ cudaError_t norm_vec(const NormParams &p, const Cut &c, int sms, cudaStream_t s)
 }
 
 // Columns one by one: 8 a thread up to 4096 columns, 16 and 32 beyond.
-RowShape elem_shape(int64_t dim, int64_t rows, int sms) {
+RowShape elem_shape(int64_t dim) {
   RowShape r;
   r.nv = dim <= 4096 ? 8 : dim <= 8192 ? 16 : 32;
   r.wpr = (int)((dim + 32 * r.nv - 1) / (32 * r.nv));
@@ -918,7 +922,7 @@ cudaError_t norm_elems(const NormParams &p, const RowShape &sh, int sms, cudaStr
 
 template <typename T, typename R, bool RES>
 cudaError_t norm_scalar(const NormParams &p, int sms, cudaStream_t s) {
-  const RowShape sh = elem_shape(p.dim, p.rows, sms);
+  const RowShape sh = elem_shape(p.dim);
   if (sh.nv == 8)
     return sh.threads <= 256 ? norm_elems<T, R, RES, 8, 256, 5>(p, sh, sms, s) : norm_elems<T, R, RES, 8, 512, 2>(p, sh, sms, s);
   return sh.nv == 16 ? norm_elems<T, R, RES, 16, 512, 1>(p, sh, sms, s) : norm_elems<T, R, RES, 32, 512, 1>(p, sh, sms, s);
@@ -1005,7 +1009,7 @@ cudaError_t bwd_elems(const NormBwdParams &p, const RowShape &sh, int sms, cudaS
 
 template <typename T, typename R, bool DRO>
 cudaError_t bwd_scalar(const NormBwdParams &p, int sms, cudaStream_t s) {
-  const RowShape sh = elem_shape(p.dim, p.rows, sms);
+  const RowShape sh = elem_shape(p.dim);
   if (sh.nv == 8)
     return sh.threads <= 256 ? bwd_elems<T, R, DRO, 8, 256, 2>(p, sh, sms, s) : bwd_elems<T, R, DRO, 8, 512, 1>(p, sh, sms, s);
   return bwd_elems<T, R, DRO, 16, 512, 1>(p, sh, sms, s);
