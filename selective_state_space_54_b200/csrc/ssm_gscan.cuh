@@ -174,8 +174,8 @@ __device__ __forceinline__ bool spun(unsigned long long &started, unsigned &n, u
 }
 
 // ---- copies ahead into shared memory ---------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {  // zeros where !in
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {  // zeros after `bytes`
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4u : 0u) : "memory");

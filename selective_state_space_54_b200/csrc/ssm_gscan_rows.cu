@@ -3,11 +3,16 @@
 //
 // Memory bound: 2 bytes a value in bf16 for each of u, f, z, y (forward) and
 // u, f, z, dout, du, df, dz (backward), against 4 and 5 special-function results a value.
-// A warp copies its next steps into shared memory ahead (cp.async: whole 16-byte pieces, or
-// 4-byte words or elements where rows are not aligned, always a contiguous run a warp), reads
+// A warp copies its next steps into shared memory ahead (cp.async: 16-byte pieces, or 4-byte
+// words or elements where the tensors themselves are not aligned, always a contiguous run a
+// warp), reads
 // 32 bytes a lane from there (a run of 16 bf16 or 8 fp32 steps), as pairs (t, t + S/2) on
 // which the gates, the two half runs and the output run as f32x2 operations; the 32 lanes'
-// runs are joined by shuffles.
+// runs are joined by shuffles.  Rows that are not whole 16-byte pieces (CUT) are cut at the
+// aligned places: the first chunk begins a few steps before its row, and steps outside the
+// row have gate 0 and are not stored.  Measured forward + backward, 2 x 5120 x 4001 bf16: 72
+// + 153 us, 125 + 266 us by elements; 2 x 1536 x 3001 fp32: 34 + 61 us, 41 + 72 us by 4-byte
+// words.  A variant of its own, as aligned rows lose 10 % to the extra tests.
 //
 // Two schedules.  k_rows_*: a warp walks its row, one 32-lane pass after another, the state
 // in a register; rows shorter than a pass share a warp.  k_tiles_*: few long rows; the eight
@@ -64,10 +69,12 @@ struct Lanes {
   int W, base, sl;
 };
 
-// Copies the row's steps [t, t + W * S) (those below L; zeros beyond) to the group's chunks.
-// mode 2: 16-byte pieces, 1: 4-byte words, 0: elements (not asynchronous).
-template <typename T>
-__device__ __forceinline__ void fill_slot(unsigned char *slot, const T *row, int64_t t, int64_t L, int mode, const Lanes &g) {
+// Copies the row's steps [t, t + W * S) (those below L; zeros beyond) to the group's chunks;
+// a negative t begins in the row before.  The row's chunks begin `early` steps before it, at
+// an aligned place.  mode 2: 16-byte pieces, 1: 4-byte words, 0: elements (not asynchronous).
+template <typename T, bool CUT>
+__device__ __forceinline__ void fill_slot(unsigned char *slot, const T *row, int64_t t, int64_t L, int early, int mode,
+                                          const Lanes &g) {
   const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
   const int n = (int)(L - t < g.W * Geo<T>::S ? L - t : g.W * Geo<T>::S);  // steps there are
   const T *src = row + t;
@@ -76,8 +83,9 @@ __device__ __forceinline__ void fill_slot(unsigned char *slot, const T *row, int
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int u = j * g.W + g.sl;
-      const bool in = u * E < n;
-      copy16(s + unit_at(g.base + (u >> 1), u & 1), in ? src + u * E : row, in);
+      // of a piece that the row's end cuts, the row's part
+      const int m = CUT ? min(max(n - u * E, 0), E) : u * E < n ? E : 0;
+      copy16(s + unit_at(g.base + (u >> 1), u & 1), m ? src + u * E : row - early, (uint32_t)(m * (int)sizeof(T)));
     }
   } else if (mode == 1) {
     constexpr int E = 4 / (int)sizeof(T);
@@ -115,7 +123,7 @@ __device__ __forceinline__ void get_chunk(uint32_t (&w)[8], const unsigned char 
 // Stores the group's steps [t, t + W * S) below L from the lanes' pairs.  Unaligned rows go
 // through `slot` (whose chunks the lanes have read) so that the warp stores contiguous runs;
 // a row's steps are written by its own lanes only, `live` being the same in all of them.
-template <typename T>
+template <typename T, bool CUT>
 __device__ __forceinline__ void put_chunk(unsigned char *slot, T *row, int64_t t, int64_t L, int mode, bool v32,
                                           const Lanes &g, const f2 (&v)[Geo<T>::H], bool live) {
   constexpr int S = Geo<T>::S, H = Geo<T>::H;
@@ -130,7 +138,17 @@ __device__ __forceinline__ void put_chunk(unsigned char *slot, T *row, int64_t t
   }
   if (mode == 2) {
     T *dst = row + t + g.sl * S;
-    const int64_t rem = live ? L - t - g.sl * S : 0;
+    const int64_t t0 = t + g.sl * S, rem = live ? L - t0 : 0;
+    if (CUT && (t0 < 0 || (rem < S && rem % (S / 2)))) {  // cut by the row's start or end: its own steps one by one
+      const int lead = t0 < 0 ? (int)-t0 : 0;
+#pragma unroll
+      for (int e = 0; e < S; ++e)
+        if (e >= lead && e < rem) {
+          if constexpr (sizeof(T) == 2) dst[e] = (T)(w[e >> 1] >> (16 * (e & 1)));
+          else dst[e] = __uint_as_float(w[e]);
+        }
+      return;
+    }
     if (v32 && rem >= S) {
       asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                    "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -152,14 +170,14 @@ __device__ __forceinline__ void put_chunk(unsigned char *slot, T *row, int64_t t
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int k = j * g.W + g.sl;
-      if (k * E < n)
+      if (k * E < n && (!CUT || k * E + t >= 0))
         __stcs(reinterpret_cast<uint32_t *>(dst + k * E), *reinterpret_cast<const uint32_t *>(slot + word_at(g.base + (k >> 3), k & 7)));
     }
   } else {
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       const int e = j * g.W + g.sl, l = e / S, k = e % S;
-      if (e < n)
+      if (e < n && (!CUT || e + t >= 0))
         dst[e] = *reinterpret_cast<const T *>(slot + word_at(g.base + l, k * (int)sizeof(T) / 4) + (k * (int)sizeof(T) & 3));
     }
   }
@@ -167,9 +185,9 @@ __device__ __forceinline__ void put_chunk(unsigned char *slot, T *row, int64_t t
 
 // bit e: a sequence starts at the lane's step e
 template <int S>
-__device__ __forceinline__ unsigned load_starts(const uint8_t *src, int64_t rem, int vec) {
+__device__ __forceinline__ unsigned load_starts(const uint8_t *src, int64_t rem, int lead, int vec) {
   unsigned m = 0;
-  if (vec && rem >= S) {
+  if (vec && rem >= S && lead == 0) {
 #pragma unroll
     for (int v = 0; v < S / 4; ++v) {
       const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src) + v);
@@ -179,7 +197,7 @@ __device__ __forceinline__ unsigned load_starts(const uint8_t *src, int64_t rem,
   } else {
 #pragma unroll
     for (int e = 0; e < S; ++e)
-      if (e < rem && src[e]) m |= 1u << e;
+      if (e >= lead && e < rem && src[e]) m |= 1u << e;
   }
   return m;
 }
@@ -192,26 +210,45 @@ constexpr int kStage = kSlot * (2 + (Z ? 1 : 0) + (BWD ? 1 : 0));
 template <bool Z>
 constexpr int kSlotG = kSlot * (Z ? 3 : 2);
 
-template <typename T, bool Z, bool BWD>
-__device__ __forceinline__ void fill_stage(unsigned char *st, const GsParams &p, int64_t row, int64_t t, const Lanes &g) {
-  const int64_t at0 = row * p.L;
-  fill_slot<T>(st + kSlotF, static_cast<const T *>(p.f) + at0, t, p.L, p.vec, g);
-  fill_slot<T>(st + kSlotU, static_cast<const T *>(p.u) + at0, t, p.L, p.vec, g);
-  if constexpr (Z) fill_slot<T>(st + kSlotZ, static_cast<const T *>(p.z) + at0, t, p.L, p.vec, g);
-  if constexpr (BWD) fill_slot<T>(st + kSlotG<Z>, static_cast<const T *>(p.dout) + at0, t, p.L, p.vec, g);
+// steps of the row's first chunk that lie before the row
+template <bool CUT>
+__device__ __forceinline__ int lead_of(const GsParams &p, int64_t row) {
+  return CUT ? (int)(row * p.L) & p.cut : 0;
 }
 
-// -g of the lane's steps; steps past the row's end leave the state alone (g = 0)
+// chunks counted from t = 0; they lie lead_of(row) steps earlier
+template <typename T, bool Z, bool BWD, bool CUT>
+__device__ __forceinline__ void fill_stage(unsigned char *st, const GsParams &p, int64_t row, int64_t t, const Lanes &g) {
+  const int64_t at0 = row * p.L;
+  const int early = lead_of<CUT>(p, row);
+  t -= early;
+  fill_slot<T, CUT>(st + kSlotF, static_cast<const T *>(p.f) + at0, t, p.L, early, p.vec, g);
+  fill_slot<T, CUT>(st + kSlotU, static_cast<const T *>(p.u) + at0, t, p.L, early, p.vec, g);
+  if constexpr (Z) fill_slot<T, CUT>(st + kSlotZ, static_cast<const T *>(p.z) + at0, t, p.L, early, p.vec, g);
+  if constexpr (BWD) fill_slot<T, CUT>(st + kSlotG<Z>, static_cast<const T *>(p.dout) + at0, t, p.L, early, p.vec, g);
+}
+
+// A chunk's first `lead` steps, which are not the row's, set to zero in every slot of a stage
+template <typename T, bool Z, bool BWD>
+__device__ __forceinline__ void drop_lead(unsigned char *stage, int lane, int lead) {
+  if (lead == 0) return;
+  for (int s = 0; s < kStage<Z, BWD>; s += kSlot)
+    for (int e = 0; e < lead; ++e)
+      *reinterpret_cast<T *>(stage + s + word_at(lane, e * (int)sizeof(T) / 4) + (e * (int)sizeof(T) & 3)) = T(0);
+}
+
+// -g of the lane's steps; steps outside the row leave the state alone (g = 0)
 template <typename T>
-__device__ __forceinline__ void lane_gates(f2 (&ng)[Geo<T>::H], const unsigned char *st, int lane, f2 b2, int64_t rem) {
+__device__ __forceinline__ void lane_gates(f2 (&ng)[Geo<T>::H], const unsigned char *st, int lane, f2 b2, int64_t rem,
+                                           int lead) {
   constexpr int H = Geo<T>::H;
   uint32_t f[8];
   get_chunk(f, st + kSlotF, lane);
 #pragma unroll
   for (int q = 0; q < H; ++q) ng[q] = neg_gate2(pair_at<T>(f, q), b2);
-  if (rem < Geo<T>::S) {
+  if (rem < Geo<T>::S || lead > 0) {
 #pragma unroll
-    for (int q = 0; q < H; ++q) ng[q] = zero_at(ng[q], q >= rem, q + H >= rem);
+    for (int q = 0; q < H; ++q) ng[q] = zero_at(ng[q], q >= rem || q < lead, q + H >= rem || q + H < lead);
   }
 }
 
@@ -278,7 +315,7 @@ __device__ __forceinline__ Run run_of(const Run &r, int lane, int W) {
 }
 
 // the lane's outputs from the state entering its first half run
-template <typename T, bool TIED, bool Z, bool ST>
+template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 __device__ __forceinline__ void lane_out(const GsParams &p, int64_t row, int64_t t, unsigned char *stage, const Lanes &g,
                                          unsigned st, const f2 (&ng)[Geo<T>::H], float hin, const Run &lo, bool live) {
   constexpr int H = Geo<T>::H;
@@ -300,7 +337,7 @@ __device__ __forceinline__ void lane_out(const GsParams &p, int64_t row, int64_t
       o[q] = h;
     }
   }
-  put_chunk<T>(stage + kSlotU, static_cast<T *>(p.y) + row * p.L, t, p.L, p.vec, p.v32, g, o, live);
+  put_chunk<T, CUT>(stage + kSlotU, static_cast<T *>(p.y) + row * p.L, t, p.L, p.vec, p.v32, g, o, live);
 }
 
 // A warp's rows: W lanes each
@@ -312,7 +349,7 @@ __device__ __forceinline__ Lanes lanes_of(int W) {
 constexpr int kRowStages = 3;  // the pass worked on and two on their way
 
 // FULL: 32 lanes a row; otherwise short rows of one chunk a lane, `short_lanes` lanes each.
-template <typename T, bool TIED, bool Z, bool ST, bool FULL>
+template <typename T, bool TIED, bool Z, bool ST, bool FULL, bool CUT>
 __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 5 : 6) k_rows_fwd(GsParams p, int short_lanes) {
   using G = Geo<T>;
   const int W = FULL ? 32 : short_lanes;
@@ -328,34 +365,37 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 5 : 6) k_rows_fw
   if (!live) row = rows - 1;            // idle lanes read the last row and write nothing
   const unsigned b = (unsigned)row / (unsigned)p.dim, d = (unsigned)row - b * (unsigned)p.dim;  // the host checks that rows fit
   const int64_t chunks = FULL ? gs_row_chunks(p.L, sizeof(T)) : 1;
+  const int early = lead_of<CUT>(p, row);
 #pragma unroll
   for (int j = 0; j < kRowStages - 1; ++j) {
-    if (j < chunks) fill_stage<T, Z, false>(ring + j * kStage<Z, false>, p, row, j * (int64_t)G::PASS, g);
+    if (j < chunks) fill_stage<T, Z, false, CUT>(ring + j * kStage<Z, false>, p, row, j * (int64_t)G::PASS, g);
     copies_commit();
   }
   const f2 b2 = splat2(p.bias ? p.bias[d] * kLog2e : 0.f);
   float carry = p.h0 ? p.h0[row] : 0.f;
   int at = 0, ahead = kRowStages - 1;
   for (int64_t k = 0; k < chunks; ++k) {
-    const int64_t t = k * G::PASS, t0 = t + (int64_t)g.sl * G::S, rem = p.L - t0;
+    const int64_t t = k * G::PASS - early, t0 = t + (int64_t)g.sl * G::S, rem = p.L - t0;
+    const int lead = CUT && t0 < 0 ? (int)-t0 : 0;
     unsigned char *stage = ring + at * kStage<Z, false>;
     if (k + kRowStages - 1 < chunks)
-      fill_stage<T, Z, false>(ring + ahead * kStage<Z, false>, p, row, t + (kRowStages - 1) * (int64_t)G::PASS, g);
+      fill_stage<T, Z, false, CUT>(ring + ahead * kStage<Z, false>, p, row, (k + kRowStages - 1) * (int64_t)G::PASS, g);
     copies_commit();
     unsigned st = 0;
-    if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, p.start_vec);
+    if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, lead, p.start_vec);
     copies_wait<kRowStages - 1>();
     __syncwarp();
     if (p.ckpt && k > 0 && lane == 0) p.ckpt[row * chunks + k] = carry;
     f2 ng[G::H];
-    lane_gates<T>(ng, stage, lane, b2, rem);
+    drop_lead<T, Z, false>(stage, lane, lead);
+    lane_gates<T>(ng, stage, lane, b2, rem, lead);
     const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
     Run r = join<ST>(hv.hi, hv.lo);
     scan_up<ST>(r, g.sl, W);
     const Run before = run_above(r, W);
     const float hin = g.sl == 0 ? carry : run_on<ST>(before, carry);
     carry = run_on<ST>(run_of(r, W - 1, W), carry);
-    lane_out<T, TIED, Z, ST>(p, row, t, stage, g, st, ng, hin, hv.lo, live);
+    lane_out<T, TIED, Z, ST, CUT>(p, row, t, stage, g, st, ng, hin, hv.lo, live);
     __syncwarp();  // every lane is done with the stage before it is filled again
     at = at + 1 == kRowStages ? 0 : at + 1;
     ahead = ahead + 1 == kRowStages ? 0 : ahead + 1;
@@ -498,7 +538,7 @@ __device__ __forceinline__ const void *tile_look(const GsParams &p, int64_t row,
 
 // Blocks stay and take tile after tile: the next tile's ticket is drawn and its steps are on
 // their way while the current one waits for the state entering it.
-template <typename T, bool TIED, bool Z, bool ST>
+template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
   using G = Geo<T>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -511,11 +551,12 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
   const Taken now = first_ticket(p.ticket, sm.ticket, chains, (unsigned)p.dim);
   if (now.id >= total) return;
   Place at = now.place;
-  fill_stage<T, Z, false>(ring, p, at.chain, ((int64_t)at.time * kGsTileWarps + w) * G::PASS, lanes);
+  fill_stage<T, Z, false, CUT>(ring, p, at.chain, ((int64_t)at.time * kGsTileWarps + w) * G::PASS, lanes);
   copies_commit();
   for (int stg = 0;; stg ^= 1) {
-    const int64_t row = at.chain, chunk = (int64_t)at.time * kGsTileWarps + w, t = chunk * G::PASS;
+    const int64_t row = at.chain, chunk = (int64_t)at.time * kGsTileWarps + w, t = chunk * G::PASS - lead_of<CUT>(p, row);
     const int64_t t0 = t + lane * G::S, rem = p.L - t0;
+    const int lead = CUT && t0 < 0 ? (int)-t0 : 0;
     unsigned char *stage = ring + stg * kStage<Z, false>;
     unsigned drawn = 0;
     if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
@@ -524,11 +565,12 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     const f2 b2 = splat2(p.bias ? p.bias[at.rest] * kLog2e : 0.f);
     const float first = at.time == 0 && p.h0 ? p.h0[row] : 0.f;
     unsigned st = 0;
-    if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
+    if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, lead, p.start_vec);
     copies_wait<0>();
     __syncwarp();
     f2 ng[G::H];
-    lane_gates<T>(ng, stage, lane, b2, rem);
+    drop_lead<T, Z, false>(stage, lane, lead);
+    lane_gates<T>(ng, stage, lane, b2, rem, lead);
     const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
     Run r = join<ST>(hv.hi, hv.lo);
     scan_up<ST>(r, lane, 32);
@@ -538,12 +580,12 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     __syncthreads();
     const Taken next = sm.ticket;
     if (next.id < total)
-      fill_stage<T, Z, false>(ring + (stg ^ 1) * kStage<Z, false>, p, next.place.chain,
+      fill_stage<T, Z, false, CUT>(ring + (stg ^ 1) * kStage<Z, false>, p, next.place.chain,
                               ((int64_t)next.place.time * kGsTileWarps + w) * G::PASS, lanes);
     copies_commit();
     const float hw = tile_in<ST, false>(p, sm, sm.run[stg], row, at.time, first, q, seen, p.last);
     if (p.ckpt && lane == 0 && chunk > 0 && chunk < chunks) p.ckpt[row * chunks + chunk] = hw;
-    lane_out<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo, t < p.L);
+    lane_out<T, TIED, Z, ST, CUT>(p, row, t, stage, lanes, st, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo, t < p.L);
     __syncwarp();
     if (next.id >= total) break;
     at = next.place;
@@ -592,7 +634,7 @@ __device__ __forceinline__ Halves grad_halves(const Halves &h, f2 R) {
 
 // The lane's gradients, from the state entering it (hin) and the gradient reaching its
 // last step from behind (pin); returns the sum of its df.
-template <typename T, bool TIED, bool Z, bool ST>
+template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int64_t t, unsigned char *stage,
                                             const Lanes &l, unsigned st, const f2 (&ng)[Geo<T>::H],
                                             const f2 (&dh)[Geo<T>::H], f2 b2, float hin, float pin, const Run &lo,
@@ -623,7 +665,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
         o[q] = mul2(mul2(pair_at<T>(g, q), h), mul2(s, k));
       }
     }
-    if constexpr (Z) put_chunk<T>(stage + kSlotZ, static_cast<T *>(p.dz) + at0, t, p.L, p.vec, p.v32, l, o, live);
+    if constexpr (Z) put_chunk<T, CUT>(stage + kSlotZ, static_cast<T *>(p.dz) + at0, t, p.L, p.vec, p.v32, l, o, live);
   }
   f2 P = pack2(run_on<ST>(ghi, pin), pin), du[H], sum = splat2(0.f);
 #pragma unroll
@@ -634,11 +676,12 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
     P = fma2(ng[q], G, G);
     if constexpr (ST) P = zero_at(P, (st >> q) & 1u, (st >> (q + H)) & 1u);
   }
-  put_chunk<T>(stage + kSlotU, static_cast<T *>(p.du) + at0, t, p.L, p.vec, p.v32, l, du, live);
-  put_chunk<T>(stage + kSlotF, static_cast<T *>(p.df) + at0, t, p.L, p.vec, p.v32, l, wt, live);
-  if (rem < S) {
+  put_chunk<T, CUT>(stage + kSlotU, static_cast<T *>(p.du) + at0, t, p.L, p.vec, p.v32, l, du, live);
+  put_chunk<T, CUT>(stage + kSlotF, static_cast<T *>(p.df) + at0, t, p.L, p.vec, p.v32, l, wt, live);
+  const int64_t lead = CUT && l.sl * S + t < 0 ? -(t + l.sl * S) : 0;
+  if (rem < S || lead > 0) {
 #pragma unroll
-    for (int q = 0; q < H; ++q) wt[q] = zero_at(wt[q], q >= rem, q + H >= rem);
+    for (int q = 0; q < H; ++q) wt[q] = zero_at(wt[q], q >= rem || q < lead, q + H >= rem || q + H < lead);
   }
 #pragma unroll
   for (int q = 0; q < H; ++q) sum = add2(sum, wt[q]);
@@ -649,7 +692,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
 
 constexpr int kRowBwdStages = 2;
 
-template <typename T, bool TIED, bool Z, bool ST, bool FULL>
+template <typename T, bool TIED, bool Z, bool ST, bool FULL, bool CUT>
 __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bwd(GsParams p, int short_lanes) {
   using G = Geo<T>;
   const int W = FULL ? 32 : short_lanes;
@@ -665,23 +708,26 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bw
   if (!live) row = rows - 1;
   const unsigned b = (unsigned)row / (unsigned)p.dim, d = (unsigned)row - b * (unsigned)p.dim;
   const int64_t chunks = FULL ? gs_row_chunks(p.L, sizeof(T)) : 1;
-  fill_stage<T, Z, true>(ring, p, row, (chunks - 1) * (int64_t)G::PASS, l);
+  const int early = lead_of<CUT>(p, row);
+  fill_stage<T, Z, true, CUT>(ring, p, row, (chunks - 1) * (int64_t)G::PASS, l);
   copies_commit();
   const f2 b2 = splat2(p.bias ? p.bias[d] * kLog2e : 0.f);
   float pc = p.dlast ? p.dlast[row] : 0.f, db = 0.f;
   int at = 0;
   for (int64_t k = chunks - 1; k >= 0; --k, at ^= 1) {
-    const int64_t t = k * G::PASS, t0 = t + (int64_t)l.sl * G::S, rem = p.L - t0;
+    const int64_t t = k * G::PASS - early, t0 = t + (int64_t)l.sl * G::S, rem = p.L - t0;
+    const int lead = CUT && t0 < 0 ? (int)-t0 : 0;
     unsigned char *stage = ring + at * kStage<Z, true>;
-    if (k > 0) fill_stage<T, Z, true>(ring + (at ^ 1) * kStage<Z, true>, p, row, t - G::PASS, l);
+    if (k > 0) fill_stage<T, Z, true, CUT>(ring + (at ^ 1) * kStage<Z, true>, p, row, (k - 1) * (int64_t)G::PASS, l);
     copies_commit();
     const float h0 = k > 0 ? p.ckpt[row * chunks + k] : (p.h0 ? p.h0[row] : 0.f);
     unsigned st = 0;
-    if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, p.start_vec);
+    if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, lead, p.start_vec);
     copies_wait<1>();
     __syncwarp();
     f2 ng[G::H], dh[G::H];
-    lane_gates<T>(ng, stage, lane, b2, rem);
+    drop_lead<T, Z, true>(stage, lane, lead);
+    lane_gates<T>(ng, stage, lane, b2, rem, lead);
     const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
     const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, stage, lane, st, ng));
     Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
@@ -691,7 +737,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bw
     const float hin = l.sl == 0 ? h0 : run_on<ST>(before, h0);
     const float pin = l.sl == W - 1 ? pc : run_on<ST>(after, pc);
     pc = run_on<ST>(run_of(g, 0, W), pc);
-    db += lane_grads<T, TIED, Z, ST>(p, row, t, stage, l, st, ng, dh, b2, hin, pin, hv.lo, gv.hi, live);
+    db += lane_grads<T, TIED, Z, ST, CUT>(p, row, t, stage, l, st, ng, dh, b2, hin, pin, hv.lo, gv.hi, live);
     __syncwarp();  // every lane is done with the stage before it is filled again
   }
   if (p.dh0 && live && l.sl == 0) p.dh0[row] = pc;
@@ -701,7 +747,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bw
   }
 }
 
-template <typename T, bool TIED, bool Z, bool ST>
+template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
   using G = Geo<T>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -716,11 +762,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
   const Taken now = first_ticket(p.ticket, sm.ticket, chains, (unsigned)p.dim);
   if (now.id >= total) return;
   Place at = now.place;
-  fill_stage<T, Z, true>(ring, p, at.chain, chunk_of(at.time) * G::PASS, lanes);
+  fill_stage<T, Z, true, CUT>(ring, p, at.chain, chunk_of(at.time) * G::PASS, lanes);
   copies_commit();
   for (int stg = 0;; stg ^= 1) {
-    const int64_t row = at.chain, chunk = chunk_of(at.time), t = chunk * G::PASS;
+    const int64_t row = at.chain, chunk = chunk_of(at.time), t = chunk * G::PASS - lead_of<CUT>(p, row);
     const int64_t t0 = t + lane * G::S, rem = p.L - t0;
+    const int lead = CUT && t0 < 0 ? (int)-t0 : 0;
     unsigned char *stage = ring + stg * kStage<Z, true>;
     unsigned drawn = 0;
     if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
@@ -730,11 +777,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     const float first = at.time == 0 && p.dlast ? p.dlast[row] : 0.f;
     const float h0 = chunk >= chunks ? 0.f : chunk > 0 ? p.ckpt[row * chunks + chunk] : (p.h0 ? p.h0[row] : 0.f);
     unsigned st = 0;
-    if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, p.start_vec);
+    if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, lead, p.start_vec);
     copies_wait<0>();
     __syncwarp();
     f2 ng[G::H], dh[G::H];
-    lane_gates<T>(ng, stage, lane, b2, rem);
+    drop_lead<T, Z, true>(stage, lane, lead);
+    lane_gates<T>(ng, stage, lane, b2, rem, lead);
     const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
     const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, stage, lane, st, ng));
     Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
@@ -747,11 +795,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     __syncthreads();
     const Taken next = sm.ticket;
     if (next.id < total)
-      fill_stage<T, Z, true>(ring + (stg ^ 1) * kStage<Z, true>, p, next.place.chain, chunk_of(next.place.time) * G::PASS,
+      fill_stage<T, Z, true, CUT>(ring + (stg ^ 1) * kStage<Z, true>, p, next.place.chain, chunk_of(next.place.time) * G::PASS,
                              lanes);
     copies_commit();
     const float pw = tile_in<ST, true>(p, sm, sm.run[stg], row, at.time, first, q, seen, p.dh0);
-    float db = lane_grads<T, TIED, Z, ST>(p, row, t, stage, lanes, st, ng, dh, b2, hin,
+    float db = lane_grads<T, TIED, Z, ST, CUT>(p, row, t, stage, lanes, st, ng, dh, b2, hin,
                                           lane == 31 ? pw : run_on<ST>(after, pw), hv.lo, gv.hi, t < p.L);
     if (p.dbias_part) {
 #pragma unroll
@@ -777,43 +825,50 @@ cudaError_t with_smem(K kern, int smem) {
   return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
 }
 
-template <typename T, bool TIED, bool Z, bool ST>
+// CUT: rows whose chunks begin at aligned places before them (p.cut); short rows take that
+// variant always.
+template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 cudaError_t launch_t(bool bwd, int path, const GsParams &p, cudaStream_t s) {
   const int64_t rows = p.batch * p.dim;
   cudaError_t e;
   if (path == SSM_PATH_LOOKBACK) {
     const int smem = kGsTileWarps * 2 * (bwd ? kStage<Z, true> : kStage<Z, false>);
-    auto kern = bwd ? k_tiles_bwd<T, TIED, Z, ST> : k_tiles_fwd<T, TIED, Z, ST>;
+    auto kern = bwd ? k_tiles_bwd<T, TIED, Z, ST, CUT> : k_tiles_fwd<T, TIED, Z, ST, CUT>;
     if ((e = with_smem(kern, smem)) != cudaSuccess) return e;
     const int64_t n = std::min<int64_t>(rows * p.tiles, (int64_t)p.sms * (bwd ? 2 : 3));
     kern<<<(unsigned)n, kTileThreads, smem, s>>>(p);
     return cudaGetLastError();
   }
   int W = 32;  // lanes per row: the fewest that hold a short row
-  while (W > 1 && (int64_t)(W / 2) * Geo<T>::S >= p.L) W /= 2;
+  while (W > 1 && (int64_t)(W / 2) * Geo<T>::S >= gs_row_span(p.L, sizeof(T))) W /= 2;
   const int64_t warps = (rows + 32 / W - 1) / (32 / W), blocks = (warps * 32 + kRowThreads - 1) / kRowThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int smem = kRowThreads / 32 * (bwd ? kRowBwdStages * kStage<Z, true> : kRowStages * kStage<Z, false>);
-  auto kern = W == 32 ? (bwd ? k_rows_bwd<T, TIED, Z, ST, true> : k_rows_fwd<T, TIED, Z, ST, true>)
-                      : (bwd ? k_rows_bwd<T, TIED, Z, ST, false> : k_rows_fwd<T, TIED, Z, ST, false>);
+  auto kern = W == 32 ? (bwd ? k_rows_bwd<T, TIED, Z, ST, true, CUT> : k_rows_fwd<T, TIED, Z, ST, true, CUT>)
+                      : (bwd ? k_rows_bwd<T, TIED, Z, ST, false, true> : k_rows_fwd<T, TIED, Z, ST, false, true>);
   if ((e = with_smem(kern, smem)) != cudaSuccess) return e;
   kern<<<(unsigned)blocks, kRowThreads, smem, s>>>(p, W);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_io(bool bwd, int path, const GsParams &p, cudaStream_t s) {
+template <typename T, bool CUT>
+cudaError_t launch_cut(bool bwd, int path, const GsParams &p, cudaStream_t s) {
   const int v = (p.untied ? 0 : 4) | (p.z ? 2 : 0) | (p.starts ? 1 : 0);
   switch (v) {
-    case 0: return launch_t<T, false, false, false>(bwd, path, p, s);
-    case 1: return launch_t<T, false, false, true>(bwd, path, p, s);
-    case 2: return launch_t<T, false, true, false>(bwd, path, p, s);
-    case 3: return launch_t<T, false, true, true>(bwd, path, p, s);
-    case 4: return launch_t<T, true, false, false>(bwd, path, p, s);
-    case 5: return launch_t<T, true, false, true>(bwd, path, p, s);
-    case 6: return launch_t<T, true, true, false>(bwd, path, p, s);
-    default: return launch_t<T, true, true, true>(bwd, path, p, s);
+    case 0: return launch_t<T, false, false, false, CUT>(bwd, path, p, s);
+    case 1: return launch_t<T, false, false, true, CUT>(bwd, path, p, s);
+    case 2: return launch_t<T, false, true, false, CUT>(bwd, path, p, s);
+    case 3: return launch_t<T, false, true, true, CUT>(bwd, path, p, s);
+    case 4: return launch_t<T, true, false, false, CUT>(bwd, path, p, s);
+    case 5: return launch_t<T, true, false, true, CUT>(bwd, path, p, s);
+    case 6: return launch_t<T, true, true, false, CUT>(bwd, path, p, s);
+    default: return launch_t<T, true, true, true, CUT>(bwd, path, p, s);
   }
+}
+
+template <typename T>
+cudaError_t launch_io(bool bwd, int path, const GsParams &p, cudaStream_t s) {
+  return p.cut ? launch_cut<T, true>(bwd, path, p, s) : launch_cut<T, false>(bwd, path, p, s);
 }
 
 }  // namespace

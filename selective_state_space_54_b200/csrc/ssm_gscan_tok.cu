@@ -113,7 +113,7 @@ __device__ __forceinline__ void fill_slot(unsigned char *slot, const T *src, int
   if (n == Tok<T>::RUN && ch == kTokChannels) {
 #pragma unroll
     for (int j = 0; j < Tok<T>::RUN / STEP; ++j) {
-      copy16(s + 512 * j, q, true);
+      copy16(s + 512 * j, q, 16u);
       q += STEP * dim;
     }
   } else {
@@ -121,7 +121,7 @@ __device__ __forceinline__ void fill_slot(unsigned char *slot, const T *src, int
 #pragma unroll 1
     for (int j = 0; j < Tok<T>::RUN / STEP; ++j) {
       const bool in = j * STEP < left;
-      copy16(s + 512 * j, in ? q : src, in);
+      copy16(s + 512 * j, in ? q : src, in ? 16u : 0u);
       q += STEP * dim;
     }
   }

@@ -18,8 +18,17 @@ ssm_status cuda_status(cudaError_t e);
 // (the first of a row is the initial state and is not read).
 constexpr int kGsLaneBytes = 32;
 __host__ __device__ __forceinline__ int gs_row_steps(int esize) { return 32 * kGsLaneBytes / esize; }
+// Rows that are not whole 16-byte pieces are cut where memory is aligned to 32 bytes (as far
+// as the tensors are): a row's first chunk begins `row * L mod the lane's steps` steps early.
+__host__ __device__ __forceinline__ int gs_row_cut(int64_t L, int esize) {  // mask of that remainder
+  return L % (16 / esize) ? kGsLaneBytes / esize - 1 : 0;
+}
+__host__ __device__ __forceinline__ int64_t gs_row_span(int64_t L, int esize) {  // steps the widest row takes
+  const int cut = gs_row_cut(L, esize);
+  return cut ? L + cut + 1 - (L & -L) : L;
+}
 __host__ __device__ __forceinline__ int64_t gs_row_chunks(int64_t L, int esize) {
-  return (L + gs_row_steps(esize) - 1) / gs_row_steps(esize);
+  return (gs_row_span(L, esize) + gs_row_steps(esize) - 1) / gs_row_steps(esize);
 }
 constexpr int kGsTileWarps = 8;    // warps, and warp runs of steps, per look-back tile
 constexpr int kGsRowGroup = 31;    // tiles between two published states of a row, at most
@@ -45,6 +54,7 @@ struct GsParams {
   int64_t batch, dim, L;
   int tok, untied;
   int vec;                           // accesses rows allow: 2 = 16 bytes, 1 = 4, 0 = one element
+  int cut;                           // channel-major: gs_row_cut
   int v32;                           // channel-major: 32-byte stores; token-major: two channels at once
   int start_vec;                     // starts rows 4-byte aligned
   // look-back schedule (zeroed): error word, ticket counter, tile runs, group states

@@ -63,9 +63,9 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   const bool tok = (s->flags & SSM_FLAG_TOKEN_MAJOR) != 0;
   const int es = (int)esize(s->io_dtype);
   const int64_t rows = s->batch * s->dim, L = s->seqlen;
-  const int64_t row_tile = (int64_t)kGsTileWarps * gs_row_steps(es);
+  const int64_t row_tiles = L == 0 ? 0 : (gs_row_chunks(L, es) + kGsTileWarps - 1) / kGsTileWarps;
   l.path = tok ? SSM_PATH_LOOKBACK : s->path;
-  if (l.path == SSM_PATH_AUTO && L <= row_tile) l.path = SSM_PATH_PER_GROUP;
+  if (l.path == SSM_PATH_AUTO && row_tiles <= 1) l.path = SSM_PATH_PER_GROUP;
   if (l.path != SSM_PATH_PER_GROUP) {
     l.sms = device_sms();
     if (l.sms <= 0) return SSM_ERR_CUDA;
@@ -73,7 +73,7 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   }
   const int64_t chains = tok ? s->batch * gs_tok_groups(s->dim) : rows;  // sequences of tiles
   const int64_t width = tok ? kTokChannels : 1;
-  if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L, es) : (L + row_tile - 1) / row_tile;
+  if (l.path == SSM_PATH_LOOKBACK) l.tiles = tok ? gs_tok_tiles(L, es) : row_tiles;
   if ((double)chains * (double)l.tiles > 2.0e9) return SSM_ERR_UNSUPPORTED;  // a grid dimension
   // Tiles between two published states (a group).  One where there are enough chains: a
   // chain's state then takes about 1.2 us from tile to tile, which the tiles of the other
@@ -126,10 +126,12 @@ cudaError_t gs_control(GsParams &p, const GsPlan &l, char *ws, cudaStream_t s) {
 
 // Widest access every given pointer and row allows: 16 bytes, 4, or one element; and whether
 // channel-major rows take 32-byte stores, token-major ones a pair of channels at once.
+// Channel-major rows that are cut at aligned places need the pointers' alignment alone.
 void gs_access(GsParams &p, size_t es, std::initializer_list<const void *> ptrs) {
   const size_t row = (size_t)(p.tok ? p.dim : p.L) * es;
+  p.cut = p.tok ? 0 : gs_row_cut(p.L, (int)es);
   auto all = [&](size_t a) {
-    if (row % a) return false;
+    if (row % a && !(p.cut && a >= 16)) return false;
     for (const void *q : ptrs)
       if (!aligned(q, a)) return false;
     return true;

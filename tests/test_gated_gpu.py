@@ -526,3 +526,40 @@ def test_queries_of_empty_shapes(cuda_device, shape, token_major):
         sh = ssm.gated_scan_shape(u, token_major=token_major, path=path)
         assert ssm.gated_scan_fwd_workspace_bytes(sh) == 0 and ssm.gated_scan_bwd_workspace_bytes(sh) == 0
         assert ssm.gated_scan_path(sh) in ssm.PATH_NAMES.values()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("path", ["per_group", "lookback"])
+@pytest.mark.parametrize("seqlen", [1, 17, 513, 2051, 4099])
+def test_saved_states_serve_differently_aligned_gradients(cuda_device, dtype, path, seqlen):
+    """Where rows are cut depends on the shape alone: states saved beside aligned tensors serve
+    a backward whose dout starts off every boundary, with the same bits; nothing outside the
+    gradients is written."""
+    import torch
+    import selective_state_space_54_b200 as ssm
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    path = ssm.SSM_PATH_PER_GROUP if path == "per_group" else ssm.SSM_PATH_LOOKBACK
+    shape = (2, 5, seqlen)
+    gen = torch.Generator(device=cuda_device).manual_seed(seqlen)
+    u, f, z, dy = (torch.randn(shape, device=cuda_device, generator=gen).to(dt) for _ in range(4))
+    bias = torch.linspace(-1, 3, 5, device=cuda_device)
+    h0 = torch.randn(2, 5, device=cuda_device, generator=gen)
+    sh = ssm.gated_scan_shape(u, save_states=True, path=path)
+    ws = torch.empty(max(ssm.gated_scan_fwd_workspace_bytes(sh), 256), dtype=torch.uint8, device=cuda_device)
+    ssm.gated_scan_fwd(u, f, z, bias, initial_state=h0, workspace=ws, save_states=True, path=path)
+    want = ssm.gated_scan_bwd(u, f, z, bias, dy, initial_state=h0, path=path, want_dinitial_state=True)
+
+    def off(fill):  # one element past a 16-byte boundary, with a guard on either side
+        whole = torch.full((u.numel() + 64,), 7.0, dtype=dt, device=cuda_device)
+        part = whole[33:33 + u.numel()].view(shape)
+        if fill is not None:
+            part.copy_(fill)
+        return whole, part
+
+    outs = {k: off(None) for k in ("du", "df", "dz")}
+    got = ssm.gated_scan_bwd(u, f, z, bias, off(dy)[1], initial_state=h0, path=path, want_dinitial_state=True,
+                             fwd_workspace=ws, out={k: v[1] for k, v in outs.items()})
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
+    for k, (whole, _) in outs.items():
+        assert bool((whole[:33] == 7).all()) and bool((whole[33 + u.numel():] == 7).all()), k
