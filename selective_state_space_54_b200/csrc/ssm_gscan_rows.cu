@@ -468,9 +468,11 @@ __device__ __forceinline__ float look_back(const GsParams &p, int64_t row, unsig
 
 constexpr int kTileThreads = 32 * kGsTileWarps;
 
+// Tickets and runs of this tile and the one before: what is written over lies two tiles back,
+// and every warp has passed a barrier since it read it, so one barrier a tile is enough.
 struct TileShared {
-  Taken ticket;
-  Run run[2][kGsTileWarps];  // of this tile and the one before: one barrier a tile is enough
+  Taken ticket[2];
+  Run run[2][kGsTileWarps];
   float in[kGsTileWarps], db[kGsTileWarps];
 };
 
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
   const Lanes lanes = {32, 0, lane};
   const unsigned chains = (unsigned)(p.batch * p.dim), total = chains * (unsigned)p.tiles;
   const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
-  const Taken now = first_ticket(p.ticket, sm.ticket, chains, (unsigned)p.dim);
+  const Taken now = first_ticket(p.ticket, sm.ticket[0], chains, (unsigned)p.dim);
   if (now.id >= total) return;
   Place at = now.place;
   fill_stage<T, Z, false, CUT>(ring, p, at.chain, ((int64_t)at.time * kGsTileWarps + w) * G::PASS, lanes);
@@ -576,9 +578,9 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     scan_up<ST>(r, lane, 32);
     const Run before = run_above(r, 32);
     if (lane == 31) sm.run[stg][w] = r;
-    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, (unsigned)p.dim);
+    if (threadIdx.x == 0) hand_out(sm.ticket[stg], drawn, chains, (unsigned)p.dim);
     __syncthreads();
-    const Taken next = sm.ticket;
+    const Taken next = sm.ticket[stg];
     if (next.id < total)
       fill_stage<T, Z, false, CUT>(ring + (stg ^ 1) * kStage<Z, false>, p, next.place.chain,
                               ((int64_t)next.place.time * kGsTileWarps + w) * G::PASS, lanes);
@@ -759,7 +761,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
   const int64_t chunks = gs_row_chunks(p.L, sizeof(T));
   // the warp's chunk of a tile taken from behind; a tile's chunks past the row's end are empty
   auto chunk_of = [&](unsigned time) { return (int64_t)(p.tiles - 1 - time) * kGsTileWarps + w; };
-  const Taken now = first_ticket(p.ticket, sm.ticket, chains, (unsigned)p.dim);
+  const Taken now = first_ticket(p.ticket, sm.ticket[0], chains, (unsigned)p.dim);
   if (now.id >= total) return;
   Place at = now.place;
   fill_stage<T, Z, true, CUT>(ring, p, at.chain, chunk_of(at.time) * G::PASS, lanes);
@@ -791,9 +793,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     const Run before = run_above(r, 32), after = run_below(g, 32);
     const float hin = lane == 0 ? h0 : run_on<ST>(before, h0);
     if (lane == 0) sm.run[stg][w] = g;
-    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, (unsigned)p.dim);
+    if (threadIdx.x == 0) hand_out(sm.ticket[stg], drawn, chains, (unsigned)p.dim);
     __syncthreads();
-    const Taken next = sm.ticket;
+    const Taken next = sm.ticket[stg];
     if (next.id < total)
       fill_stage<T, Z, true, CUT>(ring + (stg ^ 1) * kStage<Z, true>, p, next.place.chain, chunk_of(next.place.time) * G::PASS,
                              lanes);

@@ -205,11 +205,12 @@ __device__ __forceinline__ void cut_at_start(Run2 &r, unsigned st) {
   }
 }
 
-// The warps' runs of this tile and the one before (so one barrier a tile is enough).  The
-// other tile's place also takes the joined runs of a group's earlier tiles, with a barrier
-// more at the tile's end.
+// The next tile's ticket and the warps' runs, of this tile and the one before: what is written
+// over lies two tiles back, and every warp has passed a barrier since it read it, so one barrier
+// a tile is enough.  The other tile's place also takes the joined runs of a group's earlier
+// tiles, with a barrier more at the tile's end.
 struct TokShared {
-  Taken ticket;
+  Taken ticket[2];
   f2 A[2][kTokWarps][32], N[2][kTokWarps][32], B[2][kTokWarps][32];
   __device__ __forceinline__ Run2 of(int k, int w, int lane) const { return {A[k][w][lane], N[k][w][lane], B[k][w][lane]}; }
   __device__ __forceinline__ void put(int k, int w, int lane, const Run2 &r) {
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned char *ring = smem + w * 2 * STAGE;
   const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
-  const Taken now = first_ticket(p.ticket, sm.ticket, chains, cgs);
+  const Taken now = first_ticket(p.ticket, sm.ticket[0], chains, cgs);
   if (now.id >= total) return;
   Place at = now.place;
   fill_stage<T, Z, false>(ring, p, Where<T, false>(p, at, w), lane);
@@ -403,9 +404,9 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     f2 ng[RUN];
     const Run2 r = warp_run<T, TIED, ST>(ng, stage, a.n, b2, st, lane);
     sm.put(stg, w, lane, r);
-    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
+    if (threadIdx.x == 0) hand_out(sm.ticket[stg], drawn, chains, cgs);
     __syncthreads();
-    const Taken next = sm.ticket;
+    const Taken next = sm.ticket[stg];
     f2 out;
     f2 h = tile_in<ST, false>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
     if (next.id < total) fill_stage<T, Z, false>(ring + (stg ^ 1) * STAGE, p, Where<T, false>(p, next.place, w), lane);
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned char *ring = smem + w * 2 * STAGE;
   const unsigned cgs = (unsigned)gs_tok_groups(p.dim), chains = (unsigned)p.batch * cgs, total = chains * (unsigned)p.tiles;
-  const Taken now = first_ticket(p.ticket, sm.ticket, chains, cgs);
+  const Taken now = first_ticket(p.ticket, sm.ticket[0], chains, cgs);
   if (now.id >= total) return;
   Place at = now.place;
   fill_stage<T, Z, true>(ring, p, Where<T, true>(p, at, w), lane);
@@ -487,9 +488,9 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     }
     sm.put(stg, w, lane, {r.A, r.N, R});
     sm.state[stg][w][lane] = r.B;
-    if (threadIdx.x == 0) hand_out(sm.ticket, drawn, chains, cgs);
+    if (threadIdx.x == 0) hand_out(sm.ticket[stg], drawn, chains, cgs);
     __syncthreads();
-    const Taken next = sm.ticket;
+    const Taken next = sm.ticket[stg];
     f2 out;
     f2 P = tile_in<ST, true>(p, sm, stg, at.chain, at.time, first, w, lane, q, seen, out);
     if (next.id < total) fill_stage<T, Z, true>(ring + (stg ^ 1) * STAGE, p, Where<T, true>(p, next.place, w), lane);
