@@ -382,7 +382,8 @@ def _workspace_for(nbytes, device, workspace):
 
 @functools.lru_cache(maxsize=256)
 def _gated_shape(batch, dim, seqlen, io_dtype, path, flags):
-    # read-only for the library (a const pointer): one struct serves every call of a shape
+    # read-only for the library (a const pointer): one struct serves every call of a shape, and
+    # so never leaves the binding (gated_scan_shape makes the caller's)
     return make_shape(batch, dim, seqlen, 1, io_dtype, path, flags=flags)
 
 
@@ -415,8 +416,10 @@ def _gated_plan(key, device_index):
 
 
 def gated_scan_shape(u, *, tied=True, save_states=False, token_major=False, path: int = SSM_PATH_AUTO) -> ssm_shape:
-    """The shape of a gated_scan_fwd / gated_scan_bwd call on ``u``, for the workspace queries."""
-    return _gated_shape(*_gated_key(u, tied, save_states, token_major, path))
+    """The shape of a gated_scan_fwd / gated_scan_bwd call on ``u``, for the workspace queries:
+    a struct of the caller's own."""
+    batch, dim, seqlen, io_dtype, path, flags = _gated_key(u, tied, save_states, token_major, path)
+    return make_shape(batch, dim, seqlen, 1, io_dtype, path, flags=flags)
 
 
 def gated_scan_fwd_workspace_bytes(shape: ssm_shape) -> int:
