@@ -31,19 +31,23 @@ struct Run {
   float A, N, B;
 };
 
-// The run applied to x.  With packed sequences (ST) a run that holds a start has A = 0
-// exactly and what came before counts for nothing, infinities and NaN included; a run
-// whose gates alone round to A = 0 is treated the same.
+// With packed sequences (ST) a run that holds a start has A = -0, and what came before it counts
+// for nothing, infinities and NaN included.  Gates make no such A: they are not negative, so a
+// product of theirs that underflows is +0, through which a NaN passes as through any other.
+constexpr float kStart = -0.f;
+__device__ __forceinline__ bool has_start(float A) { return __float_as_uint(A) == 0x80000000u; }
+
+// The run applied to x.
 template <bool ST>
 __device__ __forceinline__ float run_on(const Run &r, float x) {
   const float far = fmaf(r.A, x, r.B), near = fmaf(r.N, x, x) + r.B;
   const float v = r.N > -0.5f ? near : far;
-  if constexpr (ST) return r.A == 0.f ? r.B : v;
+  if constexpr (ST) return has_start(r.A) ? r.B : v;
   return v;
 }
 
-// Two runs joined, `own` the one on the side the result comes out of: a start in it
-// stays a start, whatever the other run holds.
+// Two runs joined, `own` the one on the side the result comes out of: a start in it stays a
+// start, whatever the other run holds, and one in the other stays one too (-0 times own's A).
 template <bool ST>
 __device__ __forceinline__ Run join(const Run &own, const Run &other) {
   Run r;
@@ -51,8 +55,8 @@ __device__ __forceinline__ Run join(const Run &own, const Run &other) {
   r.A = own.A * other.A;
   r.N = fmaf(other.A, own.N, other.N);
   if constexpr (ST) {
-    if (own.A == 0.f) {
-      r.A = 0.f;
+    if (has_start(own.A)) {
+      r.A = kStart;
       r.N = -1.f;
     }
   }
@@ -126,9 +130,10 @@ __device__ __forceinline__ unsigned as_word(float v) {
   return b == 0xffffffffu ? 0x80000000u /* ~0x7fffffff, a NaN */ : ~b;
 }
 __device__ __forceinline__ float of_word(unsigned w) { return __uint_as_float(~w); }
-// A run as 64 bits: B, and N (> -1/2) or else A as a number without a sign.
+// A run as 64 bits: B, and N (> -1/2) with its sign, or else A without one, which is at most 1/2
+// then: a 2 stands for a start.
 __device__ __forceinline__ void put_run(unsigned long long *p, const Run &r) {
-  const float e = r.N > -0.5f ? -fabsf(r.N) : fabsf(r.A);
+  const float e = r.N > -0.5f ? -fabsf(r.N) : has_start(r.A) ? 2.f : fabsf(r.A);
   const unsigned long long v = ((unsigned long long)as_word(r.B) << 32) | as_word(e);
   asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
@@ -136,9 +141,9 @@ __device__ __forceinline__ Run of_words(unsigned long long v) {
   Run r;
   const float e = of_word((unsigned)v);
   r.B = of_word((unsigned)(v >> 32));
-  const bool n = (__float_as_uint(e) >> 31) != 0u;
-  r.N = n ? e : e - 1.f;
-  r.A = n ? 1.f + e : e;
+  const bool n = (__float_as_uint(e) >> 31) != 0u, start = e == 2.f;
+  r.N = n ? e : start ? -1.f : e - 1.f;
+  r.A = n ? 1.f + e : start ? kStart : e;
   return r;
 }
 __device__ __forceinline__ void put_state(unsigned *p, float h) {

@@ -272,7 +272,7 @@ __device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const unsi
   }
   if constexpr (ST) {  // a start cuts the run, whatever its later gates hold (NaN times 0)
     const bool lo = (st & ((1u << H) - 1u)) != 0u, hi = (st >> H) != 0u;
-    A = put_at(A, lo, hi, 0.f);
+    A = put_at(A, lo, hi, kStart);
     N = put_at(N, lo, hi, -1.f);
   }
   Halves h;

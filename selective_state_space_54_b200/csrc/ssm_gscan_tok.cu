@@ -199,7 +199,7 @@ template <bool ST>
 __device__ __forceinline__ void cut_at_start(Run2 &r, unsigned st) {
   if constexpr (ST) {
     if (st) {
-      r.A = splat2(0.f);
+      r.A = splat2(kStart);
       r.N = splat2(-1.f);
     }
   }
