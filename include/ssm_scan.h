@@ -322,8 +322,9 @@ ssm_status ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int
  * with a bounded wait; AUTO picks; the others return SSM_ERR_UNSUPPORTED.
  * With tied gates f = +inf leaves a finite state as it was (a padded step) and
  * f = -inf forgets it.  Arithmetic and states are fp32; a step rounds relative
- * to the larger of |h_{t-1}| and |u_t|, and memories of 1e5 steps keep their
- * length (1 - a is never formed from a).  The order of every sum is fixed:
+ * to the larger of |h_{t-1}| and |u_t|, memories of 1e5 steps keep their length
+ * (1 - a is never formed from a), and nearly closed gates their factor (a is
+ * never formed from 1 - a below 1/33).  The order of every sum is fixed:
  * repeated calls give equal bits.  An infinite state may become NaN.
  * y may not alias an input; last_state may be initial_state.  seqlen 0 copies
  * initial_state to last_state.

@@ -36,11 +36,18 @@ __global__ void __launch_bounds__(kStepThreads) k_gs_step(GsStepParams p) {
     if (p.bias) bv[0] = p.bias[d];
   }
   float o[8];
+  // channels in pairs; a single one goes with itself
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float ng = -rcp_approx(1.f + ex2(fmaf(fv[k], kLog2e, p.bias ? bv[k] * kLog2e : 0.f)));
-    hv[k] = p.untied ? fmaf(ng, hv[k], hv[k]) + uv[k] : fmaf(ng, -uv[k], fmaf(ng, hv[k], hv[k]));
+  for (int k = 0; k < N; k += 2) {
+    constexpr int J = VEC ? 1 : 0;
+    const f2 b2 = p.bias ? mul2(pack2(bv[k], bv[k + J]), splat2(kLog2e)) : splat2(0.f);
+    const f2 c = signed_gate2(pack2(fv[k], fv[k + J]), b2), h = pack2(hv[k], hv[k + J]), u = pack2(uv[k], uv[k + J]);
+    float lo, hi;
+    unpack2(p.untied ? state_step<false, true>(h, c, u) : state_step<true, true>(h, c, u), lo, hi);
+    hv[k] = lo;
+    hv[k + J] = hi;
     o[k] = z ? hv[k] * silu_fast(zv[k]) : hv[k];
+    o[k + J] = z ? hv[k + J] * silu_fast(zv[k + J]) : hv[k + J];
   }
   if constexpr (VEC) {
     IO<float>::store8(p.state, i, i + 8, true, hv);

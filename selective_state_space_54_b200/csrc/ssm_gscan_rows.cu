@@ -2,7 +2,8 @@
 // channel of one batch element) is contiguous in time.
 //
 // Memory bound: 2 bytes a value in bf16 for each of u, f, z, y (forward) and
-// u, f, z, dout, du, df, dz (backward), against 4 and 5 special-function results a value.
+// u, f, z, dout, du, df, dz (backward), against 4 and 6 special-function results a value (2 for the
+// gate, 2 for SiLU's sigmoid, which the backward's two walks form each for themselves).
 // A warp copies its next steps into shared memory ahead (cp.async: 16-byte pieces, or 4-byte
 // words or elements where the tensors themselves are not aligned, always a contiguous run a
 // warp), reads
@@ -45,15 +46,6 @@ __device__ __forceinline__ float at(const uint32_t *w, int i) {
 template <typename T>
 __device__ __forceinline__ f2 pair_at(const uint32_t *w, int q) {
   return pack2(at<T>(w, q), at<T>(w, q + Geo<T>::H));
-}
-
-// u as the state's step takes it (see state_step): the signs of a chunk's values turned
-template <typename T, bool TIED>
-__device__ __forceinline__ void as_input(uint32_t (&w)[8]) {
-  if constexpr (TIED) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] ^= sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
-  }
 }
 
 // ---- a warp's piece of one tensor in shared memory: 32 chunks of 32 bytes -------------
@@ -237,39 +229,58 @@ __device__ __forceinline__ void drop_lead(unsigned char *stage, int lane, int le
       *reinterpret_cast<T *>(stage + s + word_at(lane, e * (int)sizeof(T) / 4) + (e * (int)sizeof(T) & 3)) = T(0);
 }
 
-// -g of the lane's steps; steps outside the row leave the state alone (g = 0)
+// The gates of the lane's steps; steps outside the row leave the state alone.  Returns whether the
+// warp has nearly closed ones.
 template <typename T>
-__device__ __forceinline__ void lane_gates(f2 (&ng)[Geo<T>::H], const unsigned char *st, int lane, f2 b2, int64_t rem,
+__device__ __forceinline__ bool lane_gates(f2 (&c)[Geo<T>::H], const unsigned char *st, int lane, f2 b2, int64_t rem,
                                            int lead) {
   constexpr int H = Geo<T>::H;
   uint32_t f[8];
   get_chunk(f, st + kSlotF, lane);
+  float least = 1.f;
 #pragma unroll
-  for (int q = 0; q < H; ++q) ng[q] = neg_gate2(pair_at<T>(f, q), b2);
+  for (int q = 0; q < H; ++q) c[q] = gate2(pair_at<T>(f, q), b2, least);
+  const bool closed = __any_sync(kAll, least < kClosed);
+  if (closed) {
+#pragma unroll
+    for (int q = 0; q < H; ++q) c[q] = signed_gate2(pair_at<T>(f, q), b2);
+  }
   if (rem < Geo<T>::S || lead > 0) {
 #pragma unroll
-    for (int q = 0; q < H; ++q) ng[q] = zero_at(ng[q], q >= rem || q < lead, q + H >= rem || q + H < lead);
+    for (int q = 0; q < H; ++q) c[q] = hold_at(c[q], q >= rem || q < lead, q + H >= rem || q + H < lead);
   }
+  return closed;
 }
 
-// The lane's two half runs from zero, the steps q and the steps q + H.
+// The lane's two half runs from zero, the steps q and the steps q + H; with BWD, R of the
+// gradient's from behind, whose d is dh.
 struct Halves {
   Run lo, hi;
 };
-template <typename T, bool TIED, bool ST>
-__device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const unsigned char *stage, int lane, unsigned st) {
+template <typename T, bool TIED, bool ST, bool BWD>
+__device__ __forceinline__ Halves lane_run(bool closed, const f2 (&c)[Geo<T>::H], const unsigned char *stage, int lane,
+                                           unsigned st, const f2 *dh, f2 &R) {
   constexpr int H = Geo<T>::H;
   uint32_t u[8];
   get_chunk(u, stage + kSlotU, lane);
-  as_input<T, TIED>(u);
   f2 A = splat2(1.f), N = splat2(0.f), B = splat2(0.f);
+  R = splat2(0.f);
+  by_gates(closed, [&](auto kind) {
+    constexpr bool C = decltype(kind)::value;
 #pragma unroll
-  for (int q = 0; q < H; ++q) {
-    if constexpr (ST) B = zero_at(B, (st >> q) & 1u, (st >> (q + H)) & 1u);
-    B = state_step<TIED>(B, ng[q], pair_at<T>(u, q));
-    N = fma2(ng[q], A, N);
-    A = fma2(ng[q], A, A);
-  }
+    for (int q = 0; q < H; ++q) {
+      if constexpr (ST) B = zero_at(B, (st >> q) & 1u, (st >> (q + H)) & 1u);
+      B = state_step<TIED, C>(B, c[q], pair_at<T>(u, q));
+      run_step<C>(A, N, c[q]);
+    }
+    if constexpr (BWD) {
+#pragma unroll
+      for (int q = H - 1; q >= 0; --q) {
+        R = grad_step<C>(add2(dh[q], R), c[q]);
+        if constexpr (ST) R = zero_at(R, (st >> q) & 1u, (st >> (q + H)) & 1u);
+      }
+    }
+  });
   if constexpr (ST) {  // a start cuts the run, whatever its later gates hold (NaN times 0)
     const bool lo = (st & ((1u << H) - 1u)) != 0u, hi = (st >> H) != 0u;
     A = put_at(A, lo, hi, kStart);
@@ -279,6 +290,8 @@ __device__ __forceinline__ Halves lane_run(const f2 (&ng)[Geo<T>::H], const unsi
   unpack2(A, h.lo.A, h.hi.A);
   unpack2(N, h.lo.N, h.hi.N);
   unpack2(B, h.lo.B, h.hi.B);
+  h.lo.N = end_run(h.lo.A, h.lo.N);
+  h.hi.N = end_run(h.hi.A, h.hi.N);
   return h;
 }
 
@@ -317,26 +330,29 @@ __device__ __forceinline__ Run run_of(const Run &r, int lane, int W) {
 // the lane's outputs from the state entering its first half run
 template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 __device__ __forceinline__ void lane_out(const GsParams &p, int64_t row, int64_t t, unsigned char *stage, const Lanes &g,
-                                         unsigned st, const f2 (&ng)[Geo<T>::H], float hin, const Run &lo, bool live) {
+                                         unsigned st, bool closed, const f2 (&c)[Geo<T>::H], float hin, const Run &lo,
+                                         bool live) {
   constexpr int H = Geo<T>::H;
   if (!p.y) return;
   const int lane = g.base + g.sl;
   f2 h = pack2(hin, run_on<ST>(lo, hin)), o[H];
   uint32_t u[8], z[8];
   get_chunk(u, stage + kSlotU, lane);
-  as_input<T, TIED>(u);
   if constexpr (Z) get_chunk(z, stage + kSlotZ, lane);
+  by_gates(closed, [&](auto kind) {
+    constexpr bool C = decltype(kind)::value;
 #pragma unroll
-  for (int q = 0; q < H; ++q) {
-    if constexpr (ST) h = zero_at(h, (st >> q) & 1u, (st >> (q + H)) & 1u);
-    h = state_step<TIED>(h, ng[q], pair_at<T>(u, q));
-    if constexpr (Z) {
-      const f2 zv = pair_at<T>(z, q);
-      o[q] = mul2(h, mul2(zv, sigmoid2(zv)));
-    } else {
-      o[q] = h;
+    for (int q = 0; q < H; ++q) {
+      if constexpr (ST) h = zero_at(h, (st >> q) & 1u, (st >> (q + H)) & 1u);
+      h = state_step<TIED, C>(h, c[q], pair_at<T>(u, q));
+      if constexpr (Z) {
+        const f2 zv = pair_at<T>(z, q);
+        o[q] = mul2(h, mul2(zv, sigmoid2(zv)));
+      } else {
+        o[q] = h;
+      }
     }
-  }
+  });
   put_chunk<T, CUT>(stage + kSlotU, static_cast<T *>(p.y) + row * p.L, t, p.L, p.vec, p.v32, g, o, live);
 }
 
@@ -386,16 +402,16 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 5 : 6) k_rows_fw
     copies_wait<kRowStages - 1>();
     __syncwarp();
     if (p.ckpt && k > 0 && lane == 0) p.ckpt[row * chunks + k] = carry;
-    f2 ng[G::H];
+    f2 c[G::H], none;
     drop_lead<T, Z, false>(stage, lane, lead);
-    lane_gates<T>(ng, stage, lane, b2, rem, lead);
-    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
+    const bool closed = lane_gates<T>(c, stage, lane, b2, rem, lead);
+    const Halves hv = lane_run<T, TIED, ST, false>(closed, c, stage, lane, st, nullptr, none);
     Run r = join<ST>(hv.hi, hv.lo);
     scan_up<ST>(r, g.sl, W);
     const Run before = run_above(r, W);
     const float hin = g.sl == 0 ? carry : run_on<ST>(before, carry);
     carry = run_on<ST>(run_of(r, W - 1, W), carry);
-    lane_out<T, TIED, Z, ST, CUT>(p, row, t, stage, g, st, ng, hin, hv.lo, live);
+    lane_out<T, TIED, Z, ST, CUT>(p, row, t, stage, g, st, closed, c, hin, hv.lo, live);
     __syncwarp();  // every lane is done with the stage before it is filled again
     at = at + 1 == kRowStages ? 0 : at + 1;
     ahead = ahead + 1 == kRowStages ? 0 : ahead + 1;
@@ -570,10 +586,10 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, lead, p.start_vec);
     copies_wait<0>();
     __syncwarp();
-    f2 ng[G::H];
+    f2 c[G::H], none;
     drop_lead<T, Z, false>(stage, lane, lead);
-    lane_gates<T>(ng, stage, lane, b2, rem, lead);
-    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
+    const bool closed = lane_gates<T>(c, stage, lane, b2, rem, lead);
+    const Halves hv = lane_run<T, TIED, ST, false>(closed, c, stage, lane, st, nullptr, none);
     Run r = join<ST>(hv.hi, hv.lo);
     scan_up<ST>(r, lane, 32);
     const Run before = run_above(r, 32);
@@ -587,7 +603,8 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
     copies_commit();
     const float hw = tile_in<ST, false>(p, sm, sm.run[stg], row, at.time, first, q, seen, p.last);
     if (p.ckpt && lane == 0 && chunk > 0 && chunk < chunks) p.ckpt[row * chunks + chunk] = hw;
-    lane_out<T, TIED, Z, ST, CUT>(p, row, t, stage, lanes, st, ng, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo, t < p.L);
+    lane_out<T, TIED, Z, ST, CUT>(p, row, t, stage, lanes, st, closed, c, lane == 0 ? hw : run_on<ST>(before, hw), hv.lo,
+                                  t < p.L);
     __syncwarp();
     if (next.id >= total) break;
     at = next.place;
@@ -595,36 +612,24 @@ __global__ void __launch_bounds__(kTileThreads, 3) k_tiles_fwd(GsParams p) {
 }
 
 // ---- backward ---------------------------------------------------------------------------
-// Per lane: -g, d (the gradient reaching h directly) and, from a walk of the states, dz
-// (stored at once) and w = (h_{t-1} - u) a g (untied h_{t-1} a g), which leave
-// du = g G and df = G w to the walk of the gradient from behind.
+// Per lane: the gates, d (the gradient reaching h directly) and, from a walk of the states, dz
+// (stored at once) and w, which leaves df to the walk of the gradient from behind.
 
-// d of the lane's steps, and the gradient's half runs from zero
-template <typename T, bool Z, bool ST>
-__device__ __forceinline__ f2 lane_grad_run(f2 (&dh)[Geo<T>::H], const unsigned char *stage, int lane, unsigned st,
-                                            const f2 (&ng)[Geo<T>::H]) {
+// d of the lane's steps
+template <typename T, bool Z>
+__device__ __forceinline__ void lane_direct(f2 (&dh)[Geo<T>::H], const unsigned char *stage, int lane) {
   constexpr int H = Geo<T>::H;
-  {
-    uint32_t g[8], z[8];
-    get_chunk(g, stage + kSlotG<Z>, lane);
-    if constexpr (Z) get_chunk(z, stage + kSlotZ, lane);
+  uint32_t g[8], z[8];
+  get_chunk(g, stage + kSlotG<Z>, lane);
+  if constexpr (Z) get_chunk(z, stage + kSlotZ, lane);
 #pragma unroll
-    for (int q = 0; q < H; ++q) {
-      dh[q] = pair_at<T>(g, q);
-      if constexpr (Z) {
-        const f2 zv = pair_at<T>(z, q);
-        dh[q] = mul2(dh[q], mul2(zv, sigmoid2(zv)));
-      }
+  for (int q = 0; q < H; ++q) {
+    dh[q] = pair_at<T>(g, q);
+    if constexpr (Z) {
+      const f2 zv = pair_at<T>(z, q);
+      dh[q] = mul2(dh[q], mul2(zv, sigmoid2(zv)));
     }
   }
-  f2 R = splat2(0.f);
-#pragma unroll
-  for (int q = H - 1; q >= 0; --q) {
-    const f2 s = add2(dh[q], R);
-    R = fma2(ng[q], s, s);
-    if constexpr (ST) R = zero_at(R, (st >> q) & 1u, (st >> (q + H)) & 1u);
-  }
-  return R;
 }
 
 // the half runs on the gradient: those on the state with R in the place of B
@@ -634,12 +639,32 @@ __device__ __forceinline__ Halves grad_halves(const Halves &h, f2 R) {
   return g;
 }
 
+// The steps of the state and of the gradient with du and df, which is G (h - u) a g (untied
+// G h a g): the product of -c (h - u), left in w by the state's step, and of what the gradient's
+// makes of G, a G where c is a -g and -g G where it is an a.  The token-major kernel, with twice
+// the steps a lane in its registers, forms them otherwise (its form here: 4 x 5120 x 8192 bf16
+// backward 513 instead of 472 us).
+template <bool TIED>
+__device__ __forceinline__ f2 state_step_bwd(f2 h, f2 c, f2 u, f2 &w) {
+  const f2 m = open2(c);
+  w = mul2(c, TIED ? fma2(h, splat2(-1.f), u) : mul2(h, splat2(-1.f)));
+  const f2 to = fma2(w, splat2(-1.f), TIED ? pick2(m, h, u) : h & m);
+  return TIED ? to : add2(to, u);
+}
+template <bool TIED>
+__device__ __forceinline__ f2 grad_step_bwd(f2 G, f2 c, f2 w, f2 &du, f2 &df) {
+  const f2 m = open2(c), near = G & m, P = fma2(c, G, near), gG = fma2(c, G, fma2(G, splat2(-1.f), near));  // gG: -g G
+  df = mul2(w, pick2(m, P, gG));
+  du = TIED ? mul2(gG, splat2(-1.f)) : G;
+  return P;
+}
+
 // The lane's gradients, from the state entering it (hin) and the gradient reaching its
 // last step from behind (pin); returns the sum of its df.
 template <typename T, bool TIED, bool Z, bool ST, bool CUT>
 __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int64_t t, unsigned char *stage,
-                                            const Lanes &l, unsigned st, const f2 (&ng)[Geo<T>::H],
-                                            const f2 (&dh)[Geo<T>::H], f2 b2, float hin, float pin, const Run &lo,
+                                            const Lanes &l, unsigned st, const f2 (&c)[Geo<T>::H],
+                                            const f2 (&dh)[Geo<T>::H], float hin, float pin, const Run &lo,
                                             const Run &ghi, bool live) {
   constexpr int H = Geo<T>::H, S = Geo<T>::S;
   const int lane = l.base + l.sl;
@@ -647,10 +672,8 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
   f2 wt[H];
   {
     f2 h = pack2(hin, run_on<ST>(lo, hin)), o[H];
-    uint32_t f[8], u[8], z[8], g[8];
-    get_chunk(f, stage + kSlotF, lane);
+    uint32_t u[8], z[8], g[8];
     get_chunk(u, stage + kSlotU, lane);
-    as_input<T, TIED>(u);
     if constexpr (Z) {
       get_chunk(z, stage + kSlotZ, lane);
       get_chunk(g, stage + kSlotG<Z>, lane);
@@ -658,9 +681,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
 #pragma unroll
     for (int q = 0; q < H; ++q) {
       if constexpr (ST) h = zero_at(h, (st >> q) & 1u, (st >> (q + H)) & 1u);
-      const f2 uv = pair_at<T>(u, q), ag = gate_slope2(pair_at<T>(f, q), b2, ng[q]);
-      wt[q] = mul2(TIED ? add2(h, uv) : h, ag);
-      h = state_step<TIED>(h, ng[q], uv);
+      h = state_step_bwd<TIED>(h, c[q], pair_at<T>(u, q), wt[q]);
       if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
         const f2 zv = pair_at<T>(z, q), s = sigmoid2(zv);
         const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
@@ -672,10 +693,7 @@ __device__ __forceinline__ float lane_grads(const GsParams &p, int64_t row, int6
   f2 P = pack2(run_on<ST>(ghi, pin), pin), du[H], sum = splat2(0.f);
 #pragma unroll
   for (int q = H - 1; q >= 0; --q) {
-    const f2 G = add2(dh[q], P);
-    du[q] = TIED ? mul2(mul2(G, ng[q]), splat2(-1.f)) : G;
-    wt[q] = mul2(G, wt[q]);
-    P = fma2(ng[q], G, G);
+    P = grad_step_bwd<TIED>(add2(dh[q], P), c[q], wt[q], du[q], wt[q]);
     if constexpr (ST) P = zero_at(P, (st >> q) & 1u, (st >> (q + H)) & 1u);
   }
   put_chunk<T, CUT>(stage + kSlotU, static_cast<T *>(p.du) + at0, t, p.L, p.vec, p.v32, l, du, live);
@@ -727,11 +745,11 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bw
     if constexpr (ST) st = load_starts<G::S>(p.starts + b * p.L + t0, rem, lead, p.start_vec);
     copies_wait<1>();
     __syncwarp();
-    f2 ng[G::H], dh[G::H];
+    f2 c[G::H], dh[G::H], R;
     drop_lead<T, Z, true>(stage, lane, lead);
-    lane_gates<T>(ng, stage, lane, b2, rem, lead);
-    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
-    const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, stage, lane, st, ng));
+    lane_direct<T, Z>(dh, stage, lane);
+    const bool closed = lane_gates<T>(c, stage, lane, b2, rem, lead);
+    const Halves hv = lane_run<T, TIED, ST, true>(closed, c, stage, lane, st, dh, R), gv = grad_halves(hv, R);
     Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
     scan_up<ST>(r, l.sl, W);
     scan_down<ST>(g, l.sl, W);
@@ -739,7 +757,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 3 : 4) k_rows_bw
     const float hin = l.sl == 0 ? h0 : run_on<ST>(before, h0);
     const float pin = l.sl == W - 1 ? pc : run_on<ST>(after, pc);
     pc = run_on<ST>(run_of(g, 0, W), pc);
-    db += lane_grads<T, TIED, Z, ST, CUT>(p, row, t, stage, l, st, ng, dh, b2, hin, pin, hv.lo, gv.hi, live);
+    db += lane_grads<T, TIED, Z, ST, CUT>(p, row, t, stage, l, st, c, dh, hin, pin, hv.lo, gv.hi, live);
     __syncwarp();  // every lane is done with the stage before it is filled again
   }
   if (p.dh0 && live && l.sl == 0) p.dh0[row] = pc;
@@ -782,11 +800,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
     if constexpr (ST) st = load_starts<G::S>(p.starts + at.batch * p.L + t0, rem, lead, p.start_vec);
     copies_wait<0>();
     __syncwarp();
-    f2 ng[G::H], dh[G::H];
+    f2 c[G::H], dh[G::H], R;
     drop_lead<T, Z, true>(stage, lane, lead);
-    lane_gates<T>(ng, stage, lane, b2, rem, lead);
-    const Halves hv = lane_run<T, TIED, ST>(ng, stage, lane, st);
-    const Halves gv = grad_halves(hv, lane_grad_run<T, Z, ST>(dh, stage, lane, st, ng));
+    lane_direct<T, Z>(dh, stage, lane);
+    const bool closed = lane_gates<T>(c, stage, lane, b2, rem, lead);
+    const Halves hv = lane_run<T, TIED, ST, true>(closed, c, stage, lane, st, dh, R), gv = grad_halves(hv, R);
     Run r = join<ST>(hv.hi, hv.lo), g = join<ST>(gv.lo, gv.hi);
     scan_up<ST>(r, lane, 32);
     scan_down<ST>(g, lane, 32);
@@ -801,7 +819,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_tiles_bwd(GsParams p) {
                              lanes);
     copies_commit();
     const float pw = tile_in<ST, true>(p, sm, sm.run[stg], row, at.time, first, q, seen, p.dh0);
-    float db = lane_grads<T, TIED, Z, ST, CUT>(p, row, t, stage, lanes, st, ng, dh, b2, hin,
+    float db = lane_grads<T, TIED, Z, ST, CUT>(p, row, t, stage, lanes, st, c, dh, hin,
                                           lane == 31 ? pw : run_on<ST>(after, pw), hv.lo, gv.hi, t < p.L);
     if (p.dbias_part) {
 #pragma unroll

@@ -2,7 +2,7 @@
 // token are contiguous, as a projection leaves them.
 //
 // Memory bound like the channel-major form.  A lane takes a pair of channels, so every
-// step is one f32x2 operation, and walks kTokRun consecutive steps; the four warps of a block
+// step is one f32x2 operation, and walks Tok<T>::RUN consecutive steps; the four warps of a block
 // split a tile of 64 channels by four such runs and join them through shared memory; tiles of
 // the same channels hand their runs on through the workspace.  Blocks stay and take tile after
 // tile: the next tile's ticket is drawn and its values are on their way into shared memory
@@ -41,19 +41,6 @@ __device__ __forceinline__ f2 pair_at(const unsigned char *slot, int i, int lane
     return pack2(bf16_lo(v), bf16_hi(v));
   } else {
     return *reinterpret_cast<const f2 *>(slot + i * Tok<T>::ROW + 8 * lane);
-  }
-}
-
-// u as the state's step takes it (see state_step)
-template <typename T, bool TIED>
-__device__ __forceinline__ f2 input_at(const unsigned char *slot, int i, int lane) {
-  if constexpr (!TIED) {
-    return pair_at<T>(slot, i, lane);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint32_t v = *reinterpret_cast<const uint32_t *>(slot + i * Tok<T>::ROW + 4 * lane) ^ 0x80008000u;
-    return pack2(bf16_lo(v), bf16_hi(v));
-  } else {
-    return pair_at<T>(slot, i, lane) ^ 0x8000000080000000ull;
   }
 }
 
@@ -351,26 +338,50 @@ __device__ __forceinline__ void fill_stage(unsigned char *st, const GsParams &p,
   if constexpr (BWD) fill_slot<T>(st + kTokG<Z>, static_cast<const T *>(p.dout) + at, a.n, a.ch, p.dim, p.vec, lane);
 }
 
-// -g of the warp's steps and their run on the state; steps past the end hold it (g = 0)
-template <typename T, bool TIED, bool ST>
-__device__ __forceinline__ Run2 warp_run(f2 (&ng)[Tok<T>::RUN], const unsigned char *stage, int n, f2 b2, unsigned st, int lane) {
+// The gates of the warp's steps and their run on the state; steps past the end hold it.  With BWD,
+// R of the gradient's run from behind, whose d is dh.
+template <typename T, bool TIED, bool ST, bool BWD>
+__device__ __forceinline__ Run2 warp_run(f2 (&c)[Tok<T>::RUN], const unsigned char *stage, int n, f2 b2, unsigned st, int lane,
+                                         const f2 *dh, f2 &R) {
+  constexpr int RUN = Tok<T>::RUN;
   Run2 r = {splat2(1.f), splat2(0.f), splat2(0.f)};
+  R = splat2(0.f);
+  float least = 1.f;
 #pragma unroll
-  for (int i = 0; i < Tok<T>::RUN; ++i) ng[i] = neg_gate2(pair_at<T>(stage + kTokF, i, lane), b2);
-  if (n < Tok<T>::RUN) {
+  for (int i = 0; i < RUN; ++i) c[i] = gate2(pair_at<T>(stage + kTokF, i, lane), b2, least);
+  const bool closed = __any_sync(kAll, least < kClosed);
+  if (closed) {
 #pragma unroll
-    for (int i = 0; i < Tok<T>::RUN; ++i)
-      if (i >= n) ng[i] = splat2(0.f);
+    for (int i = 0; i < RUN; ++i) c[i] = signed_gate2(pair_at<T>(stage + kTokF, i, lane), b2);
   }
+  if (n < RUN) {
 #pragma unroll
-  for (int i = 0; i < Tok<T>::RUN; ++i) {
-    if constexpr (ST) {
-      if ((st >> i) & 1u) r.B = splat2(0.f);
+    for (int i = 0; i < RUN; ++i) c[i] = hold_at(c[i], i >= n, i >= n);
+  }
+  by_gates(closed, [&](auto kind) {
+    constexpr bool C = decltype(kind)::value;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      if constexpr (ST) {
+        if ((st >> i) & 1u) r.B = splat2(0.f);
+      }
+      r.B = state_step<TIED, C>(r.B, c[i], pair_at<T>(stage + kTokU, i, lane));
+      run_step<C>(r.A, r.N, c[i]);
     }
-    r.B = state_step<TIED>(r.B, ng[i], input_at<T, TIED>(stage + kTokU, i, lane));
-    r.N = fma2(ng[i], r.A, r.N);
-    r.A = fma2(ng[i], r.A, r.A);
-  }
+    if constexpr (BWD) {
+#pragma unroll
+      for (int i = RUN - 1; i >= 0; --i) {
+        R = grad_step<C>(add2(dh[i], R), c[i]);
+        if constexpr (ST) {
+          if ((st >> i) & 1u) R = splat2(0.f);
+        }
+      }
+    }
+  });
+  float a0, a1, n0, n1;
+  unpack2(r.A, a0, a1);
+  unpack2(r.N, n0, n1);
+  r.N = pack2(end_run(a0, n0), end_run(a1, n1));
   cut_at_start<ST>(r, st);
   return r;
 }
@@ -401,8 +412,8 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     const unsigned st = warp_starts<T, ST>(p, a.tok, a.n, lane);
     copies_wait<0>();
     __syncwarp();
-    f2 ng[RUN];
-    const Run2 r = warp_run<T, TIED, ST>(ng, stage, a.n, b2, st, lane);
+    f2 c[RUN], none;
+    const Run2 r = warp_run<T, TIED, ST, false>(c, stage, a.n, b2, st, lane, nullptr, none);
     sm.put(stg, w, lane, r);
     if (threadIdx.x == 0) hand_out(sm.ticket[stg], drawn, chains, cgs);
     __syncthreads();
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
           if constexpr (ST) {
             if ((st >> i) & 1u) h = splat2(0.f);
           }
-          h = state_step<TIED>(h, ng[i], input_at<T, TIED>(stage + kTokU, i, lane));
+          h = state_step<TIED, true>(h, c[i], pair_at<T>(stage + kTokU, i, lane));
           f2 o = h;
           if constexpr (Z) {
             const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
@@ -438,6 +449,27 @@ __global__ void __launch_bounds__(kTokThreads, kTokFwdBlocks) k_tok_fwd(GsParams
     at = next.place;
     if (p.group > 1) __syncthreads();  // every warp is done with the group's runs
   }
+}
+
+// The step of the state with w = -(h - u) a g (untied -h a g), a g being g - g^2 or a - a^2, and the
+// step of the gradient with du = g G (untied G) and df = -w G.  That one's choice by the sign of c is
+// a product with 1 or 0: fewer registers than a mask (8 x 4096 x 2048 packed backward 267 us, with
+// masks 286, and 288 as the channel-major kernels form them).
+template <bool TIED>
+__device__ __forceinline__ f2 state_step_bwd(f2 h, f2 c, f2 u, f2 &w) {
+  const f2 n = c | 0x8000000080000000ull;
+  w = mul2(TIED ? fma2(u, splat2(-1.f), h) : h, fma2(n, n, n));
+  return state_step<TIED, true>(h, c, u);
+}
+template <bool TIED>
+__device__ __forceinline__ f2 grad_step_bwd(f2 G, f2 c, f2 w, f2 &du, f2 &df) {
+  float lo, hi;
+  asm("set.lt.f32.s32 %0, %1, 0;" : "=f"(lo) : "r"((int)(unsigned)c));
+  asm("set.lt.f32.s32 %0, %1, 0;" : "=f"(hi) : "r"((int)(unsigned)(c >> 32)));
+  const f2 near = mul2(G, pack2(lo, hi)), nG = mul2(G, splat2(-1.f));
+  du = TIED ? fma2(c, nG, fma2(near, splat2(-1.f), G)) : G;
+  df = mul2(nG, w);
+  return fma2(c, G, near);
 }
 
 template <typename T, bool TIED, bool Z, bool ST>
@@ -470,22 +502,16 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
     copies_wait<0>();
     __syncwarp();
     // the state's run, and the gradient's from behind, which shares A and N with it
-    f2 ng[RUN], dh[RUN];
-    const Run2 r = warp_run<T, TIED, ST>(ng, stage, a.n, b2, st, lane);
-    f2 R = splat2(0.f);
+    f2 c[RUN], dh[RUN], R;
 #pragma unroll
-    for (int i = RUN - 1; i >= 0; --i) {
+    for (int i = 0; i < RUN; ++i) {
       dh[i] = pair_at<T>(stage + kTokG<Z>, i, lane);
       if constexpr (Z) {
         const f2 zv = pair_at<T>(stage + kTokZ, i, lane);
         dh[i] = mul2(dh[i], mul2(zv, sigmoid2(zv)));
       }
-      const f2 s = add2(dh[i], R);
-      R = fma2(ng[i], s, s);
-      if constexpr (ST) {
-        if ((st >> i) & 1u) R = splat2(0.f);
-      }
     }
+    const Run2 r = warp_run<T, TIED, ST, true>(c, stage, a.n, b2, st, lane, dh, R);
     sm.put(stg, w, lane, {r.A, r.N, R});
     sm.state[stg][w][lane] = r.B;
     if (threadIdx.x == 0) hand_out(sm.ticket[stg], drawn, chains, cgs);
@@ -510,10 +536,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
         if constexpr (ST) {
           if ((st >> i) & 1u) h = splat2(0.f);
         }
-        const f2 uv = input_at<T, TIED>(stage + kTokU, i, lane);
-        const f2 ag = gate_slope2(pair_at<T>(stage + kTokF, i, lane), b2, ng[i]);
-        wt[i] = mul2(TIED ? add2(h, uv) : h, ag);
-        h = state_step<TIED>(h, ng[i], uv);
+        h = state_step_bwd<TIED>(h, c[i], pair_at<T>(stage + kTokU, i, lane), wt[i]);
         if constexpr (Z) {  // dz = dout h s (1 + z (1 - s))
           const f2 zv = pair_at<T>(stage + kTokZ, i, lane), s = sigmoid2(zv);
           const f2 k = fma2(zv, fma2(s, splat2(-1.f), splat2(1.f)), splat2(1.f));
@@ -527,11 +550,11 @@ __global__ void __launch_bounds__(kTokThreads, kTokBwdBlocks) k_tok_bwd(GsParams
         du -= p.dim;
         df -= p.dim;
         const bool in = i < a.n;
-        const f2 G = add2(dh[i], P), d = mul2(G, wt[i]);
-        put_pair<T>(du, ch, all, in, TIED ? mul2(G, mul2(ng[i], splat2(-1.f))) : G);
-        put_pair<T>(df, ch, all, in, d);
-        if (all || in) sum = add2(sum, d);
-        P = fma2(ng[i], G, G);
+        f2 du_i, df_i;
+        P = grad_step_bwd<TIED>(add2(dh[i], P), c[i], wt[i], du_i, df_i);
+        put_pair<T>(du, ch, all, in, du_i);
+        put_pair<T>(df, ch, all, in, df_i);
+        if (all || in) sum = add2(sum, df_i);
         if constexpr (ST) {
           if ((st >> i) & 1u) P = splat2(0.f);
         }
