@@ -426,6 +426,11 @@ ssm_status ssm_scan_check(void *workspace, ssm_stream_t stream);
 ssm_status ssm_scan_test_wait_timeout(void *workspace, size_t ws_bytes,
                                       int64_t timeout_us, ssm_stream_t stream);
 
+/* The same for the wait of the gated recurrence's tiles (ssm_gated_scan_fwd
+ * and _bwd under SSM_PATH_LOOKBACK), which is another one. */
+ssm_status ssm_gated_scan_test_wait_timeout(void *workspace, size_t ws_bytes,
+                                            int64_t timeout_us, ssm_stream_t stream);
+
 /* Test hook for callers' error paths: the next `count` calls of
  * ssm_scan_fwd, ssm_scan_bwd, ssm_scan_step, ssm_causal_conv1d and
  * ssm_causal_conv1d_bwd (ssm_scan_fwd_noalloc included), and of the

@@ -43,7 +43,7 @@ EXPORTS = (
     "ssm_causal_conv1d", "ssm_causal_conv1d_bwd", "ssm_scan_test_fail_next",
     "ssm_scan_test_noalloc_reset_cycle",
     "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step", "ssm_gated_scan_path",
-    "ssm_gated_scan_fwd_workspace_bytes", "ssm_gated_scan_bwd_workspace_bytes",
+    "ssm_gated_scan_fwd_workspace_bytes", "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_scan_test_wait_timeout",
     "ssm_layer_norm", "ssm_layer_norm_bwd", "ssm_layer_norm_bwd_workspace_bytes",
 )
 
@@ -112,6 +112,8 @@ def load(path: str | None = None):
     lib.ssm_scan_check.restype = ci
     lib.ssm_scan_test_wait_timeout.argtypes = [vp, sz, i64, vp]
     lib.ssm_scan_test_wait_timeout.restype = ci
+    lib.ssm_gated_scan_test_wait_timeout.argtypes = [vp, sz, i64, vp]
+    lib.ssm_gated_scan_test_wait_timeout.restype = ci
     lib.ssm_scan_test_fail_next.argtypes = [i32]
     lib.ssm_scan_test_fail_next.restype = None
     lib.ssm_scan_test_noalloc_reset_cycle.argtypes = []

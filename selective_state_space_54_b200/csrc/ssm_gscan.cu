@@ -81,6 +81,16 @@ __global__ void __launch_bounds__(1024) k_gs_dbias(const float *part, float *out
   if (threadIdx.x == 0 && dd < dim) out[dd] = t;
 }
 
+// The tiles' wait on its own (a test hook): two warps, each thread at one of 8 words
+// that nothing sets.
+__global__ void __launch_bounds__(64) k_gs_wait_probe(const unsigned long long *words, unsigned *err,
+                                                      unsigned long long limit_ns) {
+  unsigned long long started = 0;
+  unsigned n = 0;
+  while (look64(words + (threadIdx.x & 7)) == 0ull)
+    if (!spun(started, n, err, limit_ns)) break;
+}
+
 template <typename T>
 cudaError_t launch_step_t(const GsStepParams &p, bool vec, cudaStream_t s) {
   const int64_t n = p.batch * p.dim, per = (int64_t)kStepThreads * (vec ? 8 : 1), blocks = (n + per - 1) / per;
@@ -106,6 +116,12 @@ cudaError_t launch_gscan_step(int io_dtype, const GsStepParams &p, cudaStream_t 
   auto a16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
   const bool vec = p.dim % 8 == 0 && a16(p.u) && a16(p.f) && a16(p.z) && a16(p.y) && a16(p.state) && a16(p.bias);
   return io_dtype == SSM_BF16 ? launch_step_t<uint16_t>(p, vec, s) : launch_step_t<float>(p, vec, s);
+}
+
+cudaError_t launch_gs_wait_probe(const unsigned long long *words, unsigned *err, unsigned long long limit_ns,
+                                 cudaStream_t s) {
+  k_gs_wait_probe<<<1, 64, 0, s>>>(words, err, limit_ns);
+  return cudaGetLastError();
 }
 
 }  // namespace ssm

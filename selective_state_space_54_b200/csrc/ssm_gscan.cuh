@@ -196,10 +196,11 @@ __device__ __forceinline__ unsigned look32(const unsigned *p) {
   return v;
 }
 
-// The bounded wait for such words: spun(started, n, err) is false once
-// kWaitLimitNs have passed or another wait of the call has given up; the error
-// word is set then, and the caller goes on with what it has.
-__device__ __forceinline__ bool spun(unsigned long long &started, unsigned &n, unsigned *err) {
+// The bounded wait for such words: spun(started, n, err) is false once the limit has passed or
+// another wait of the call has given up; the error word is set then, and the caller goes on with
+// what it has.
+__device__ __forceinline__ bool spun(unsigned long long &started, unsigned &n, unsigned *err,
+                                     unsigned long long limit_ns = kWaitLimitNs) {
   if (n++ == 0) {
     started = global_ns();
     return true;
@@ -207,7 +208,7 @@ __device__ __forceinline__ bool spun(unsigned long long &started, unsigned &n, u
   __nanosleep(20);
   if ((n & 63u) != 0) return true;
   if (look32(err) != 0u) return false;
-  if (global_ns() - started > kWaitLimitNs) {
+  if (global_ns() - started > limit_ns) {
     atomicOr(err, kErrWaitTimeout);
     return false;
   }

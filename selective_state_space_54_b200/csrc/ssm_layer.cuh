@@ -90,6 +90,9 @@ struct GsStepParams {
   int untied;
 };
 cudaError_t launch_gscan_step(int io_dtype, const GsStepParams &p, cudaStream_t s);
+// test hook: the tiles' bounded wait on 8 words that stay 0
+cudaError_t launch_gs_wait_probe(const unsigned long long *words, unsigned *err, unsigned long long limit_ns,
+                                 cudaStream_t s);
 
 struct NormParams {
   const void *x, *res;               // [rows][dim] io dtype, residual dtype (nullable)

@@ -294,6 +294,19 @@ ssm_status ssm_gated_scan_step(const ssm_shape *shape, const void *u, const void
   return cuda_status(launch_gscan_step(shape->io_dtype, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+ssm_status ssm_gated_scan_test_wait_timeout(void *workspace, size_t ws_bytes, int64_t timeout_us,
+                                            ssm_stream_t stream) {
+  if (!workspace || ws_bytes < kHeaderBytes || !aligned(workspace, 256)) return SSM_ERR_WORKSPACE;
+  if (timeout_us < 1 || timeout_us > 1000000) return SSM_ERR_INVALID_ARG;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  const cudaError_t e = cudaMemsetAsync(ws, 0, kHeaderBytes, s);
+  if (e != cudaSuccess) return cuda_status(e);
+  // the words at byte 64 of the zeroed header are never set
+  return cuda_status(launch_gs_wait_probe(reinterpret_cast<unsigned long long *>(ws + 64),
+                                          reinterpret_cast<unsigned *>(ws), (unsigned long long)timeout_us * 1000ull, s));
+}
+
 static ssm_status check_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t residual_dtype, float eps) {
   if (rows < 0 || dim < 0 || !(eps >= 0.f) || std::isinf(eps)) return SSM_ERR_INVALID_ARG;
   if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
