@@ -2,8 +2,8 @@
 // channel of one batch element) is contiguous in time.
 //
 // Memory bound: 2 bytes a value in bf16 for each of u, f, z, y (forward) and
-// u, f, z, dout, du, df, dz (backward), against 4 and 6 special-function results a value (2 for the
-// gate, 2 for SiLU's sigmoid, which the backward's two walks form each for themselves).
+// u, f, z, dout, du, df, dz (backward), against 4 special-function results a value (2 for the gate, 2
+// for SiLU's sigmoid), 6 in the backward's tiles, whose two walks form the sigmoid each for themselves.
 // A warp copies its next steps into shared memory ahead (cp.async: 16-byte pieces, or 4-byte
 // words or elements where the tensors themselves are not aligned, always a contiguous run a
 // warp), reads
@@ -11,9 +11,10 @@
 // which the gates, the two half runs and the output run as f32x2 operations; the 32 lanes'
 // runs are joined by shuffles.  Rows that are not whole 16-byte pieces (CUT) are cut at the
 // aligned places: the first chunk begins a few steps before its row, and steps outside the
-// row have gate 0 and are not stored.  Measured forward + backward, 2 x 5120 x 4001 bf16: 72
-// + 153 us, 125 + 266 us by elements; 2 x 1536 x 3001 fp32: 34 + 61 us, 41 + 72 us by 4-byte
-// words.  A variant of its own, as aligned rows lose 10 % to the extra tests.
+// row have gate 0 and are not stored.  Measured forward + backward, 2 x 5120 x 4001 bf16: 82
+// + 164 us, and 144 + 311 us from tensors off a 4-byte boundary, which go by elements; 2 x 1536 x 3001
+// fp32: 32 + 64 us, 45 + 79 us by 4-byte words.  A variant of its own, as aligned rows lose 10 % to
+// the extra tests.
 //
 // Two schedules.  k_rows_*: a warp walks its row, one 32-lane pass after another, the state
 // in a register; rows shorter than a pass share a warp.  k_tiles_*: few long rows; the eight

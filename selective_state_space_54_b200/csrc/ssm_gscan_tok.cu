@@ -1,7 +1,8 @@
 // Gated recurrence, token-major activations [batch][L][dim]: the channels of one
 // token are contiguous, as a projection leaves them.
 //
-// Memory bound like the channel-major form.  A lane takes a pair of channels, so every
+// Memory bound like the channel-major form, against 4 special-function results a value (backward 6: both
+// walks form SiLU's sigmoid).  A lane takes a pair of channels, so every
 // step is one f32x2 operation, and walks Tok<T>::RUN consecutive steps; the four warps of a block
 // split a tile of 64 channels by four such runs and join them through shared memory; tiles of
 // the same channels hand their runs on through the workspace.  Blocks stay and take tile after

@@ -54,8 +54,8 @@ struct GsPlan {
 // AUTO, channel-major: a warp per row needs enough rows to keep the memory system busy
 // (each holds two passes of its row in flight); with fewer, rows longer than one tile
 // are split into tiles.  Measured with z, rows as they are and in tiles, forward + backward:
-// 256 x 65536 bf16 111 + 182 us and 43 + 76 us, 768 x 262144 497 + 918 and 354 + 725 us,
-// 1024 x 2^20 1971 + 3642 and 1848 + 3806 us (fp32 x 65536: 207 + 353 and 190 + 376 us).
+// 256 x 65536 bf16 117 + 193 us and 45 + 81 us, 768 x 262144 532 + 944 and 382 + 785 us,
+// 1024 x 2^20 2104 + 3747 and 1987 + 4135 us (fp32 x 65536: 213 + 379 and 221 + 447 us).
 constexpr int64_t kRowsPerSm = 8;
 
 ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
@@ -79,13 +79,14 @@ ssm_status gs_plan(const ssm_shape *s, bool bwd, GsPlan *out) {
   // chain's state then takes about 1.2 us from tile to tile, which the tiles of the other
   // chains fill.  With fewer the chain itself would set the pace, and the tiles of a group
   // hand on their runs first (a state every group), which costs each tile a look at all of
-  // them.  Measured forward, bf16: channel-major 64 x 262144 75 us with single tiles, 90 us
-  // with groups of 31; token-major 64 chains (4096 channels x 32768) 407 and 311 us (groups
-  // of 8), 128 chains equal, 4 chains (256 x 65536) 643 and 72 us (groups of 32).
+  // them.  Measured forward, bf16: channel-major 64 x 262144 66 us with single tiles, 85 us
+  // with groups of 8; token-major 64 chains (4096 channels x 32768) 444 and 362 us (groups
+  // of 8), 128 chains equal, 4 chains (256 x 65536) 658 and 85 us (groups of 32).
   if (l.path == SSM_PATH_LOOKBACK && chains > 0 && chains < (tok ? 96 : 48))
     l.group = std::min<int64_t>(tok ? kTokGroup : kGsRowGroup, (512 + chains - 1) / chains);
   l.groups = (l.tiles + l.group - 1) / l.group;
   l.part_rows = s->batch * (l.path == SSM_PATH_LOOKBACK ? l.tiles : 1);
+  // in the backward always: with the flag too fwd_workspace may be null, which no query sees
   const bool save = bwd || (s->flags & SSM_FLAG_SAVE_STATES);
   if (save)
     l.ckpt_bytes = round_up(sizeof(float) * (size_t)rows * (size_t)(tok ? gs_tok_tiles(L, es) : gs_row_chunks(L, es)), 256);

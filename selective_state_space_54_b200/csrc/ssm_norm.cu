@@ -14,10 +14,10 @@
 // the row's share of a thread: reductions, barriers, addresses, w and b.  So the forward takes
 // two rows at a time where the registers allow.  Measured and dropped: rows copied ahead by
 // cp.async (16-byte copies of fp32 rows read every sector twice: 170 against 136 us at
-// 16384 x 4096 on an fp32 residual), w and b read from L1 for every single row (L1 at 70 %).
+// 16384 x 4096 on an fp32 residual), w and b read from L1 for every single row.
 // Rows wider than 16384 (backward 8192) take walks over memory.  Forward and backward of the
-// measured copy rate (6.46 TB/s): 32768 x 4096 bf16 105 us, 79 %; 16384 x 4096 bf16 on an
-// fp32 residual 330 us, 88 % of the 291 us that the two calls' own accesses take.
+// measured copy rate (6.46 TB/s): 32768 x 4096 bf16 110 us, 76 %; 16384 x 4096 bf16 on an
+// fp32 residual 343 us, 85 % of the 291 us that the two calls' own accesses take.
 #include "ssm_layer.cuh"
 
 #include <algorithm>
@@ -991,7 +991,9 @@ cudaError_t bwd_vec(const NormBwdParams &p, const Cut &c, int sms, cudaStream_t 
     return bwd_rows<T, R, DRO, 1, 4, 512, 1>(p, c, sh, sms, s);
   }
   if (sh.threads <= 256) return bwd_rows<T, R, DRO, 2, 2, 256, WIDE ? 1 : 2>(p, c, sh, sms, s);
-  if constexpr (WIDE) {  // 204 registers a thread: none spills
+  // Up to 5120 columns 168 registers a thread; more columns take 512 threads at 128, which spill 324 to
+  // 436 bytes each (16384 x 5120 bf16 224 us, 16384 x 6144 536 us).
+  if constexpr (WIDE) {
     if (sh.threads <= 320) return bwd_rows<T, R, DRO, 2, 4, 320, 1>(p, c, sh, sms, s);
   }
   return bwd_rows<T, R, DRO, 2, 4, 512, 1>(p, c, sh, sms, s);
